@@ -271,3 +271,11 @@ def chunk_prefill(q, k, v, log_g, beta, h0=None, cu_seqlens=None, chunk=64, out_
     route = call(q, k, v, log_g, beta, h0, out, hf, B, T, Hk, Hv, dk, dv, chunk,
                  cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
     return out, hf, route
+
+
+# ---- training entry points (include/gdn_train.h) ---------------------------
+from .train import (  # noqa: E402,F401
+    CKPT8_GROUP, GDN_E4M3, TRAIN_SIGNATURES, chunk_backward, ckpt8_load, ckpt8_store,
+    gdn_backward_workspace_bytes, gdn_chunk_backward, gdn_ckpt8_load, gdn_ckpt8_store, gdn_norm_backward,
+    gdn_norm_forward, gdn_norm_workspace_bytes, norm_backward, norm_forward,
+)

@@ -198,6 +198,9 @@ int hip_failure(const char* what, hipError_t e)
     set_route("%s failed: %s", what, hipGetErrorString(e));
     return GDN_ERR_HIP;
 }
+int refuse_call(int status, const char* who, const char* why) { return refuse(status, who, why); }
+void route_call(const Geometry& g, const char* note) { route_geometry(g, note); }
+int launch_status(hipError_t e) { return launched(e); }
 }  // namespace gdn
 
 extern "C" {

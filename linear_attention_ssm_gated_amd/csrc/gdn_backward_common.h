@@ -1,0 +1,122 @@
+// What the two routes of the delta rule's backward pass share: the chunk
+// table, the rows of a chunk and its gates.
+//
+// Notation, per chunk of C = 64 rows of one v-head, with start state h
+// (dk x dv) and the gradient dh' of its end state; G the running sum of log_g
+// in the chunk, ga_r = exp(G_r), E_s = exp(G_L - G_s), Gam_rs = exp(G_r - G_s):
+//   B = strict_lower(Gam o K K^T),  P = lower(Gam o Q K^T)
+//   T = (I + B diag(beta))^-1,  u = T (V - ga K h),  delta = beta u
+//   o = ga Q h + P delta,  h' = ga_L h + K^T E delta
+// (with beta on the right of B, beta = 0 needs no division anywhere).  With
+//   W = E beta T (ga K),  U = E beta T V,  Qt = ga Q - P beta T (ga K)
+// the states and their gradients walk the chunks by
+//   h' = ga_L h + K^T (U - W h),   dh = ga_L dh' + Qt^T do - W^T (K dh')
+// and each chunk's gradients follow from h and dh' alone:
+//   ddelta = P^T do + E K dh',  dx = T^T (beta ddelta),  dv = dx
+//   Zu = strict_lower(dx u^T),  dB = -Zu beta_s,  dP = lower(do u^T) beta_s
+//   dq = ga (do h^T) + (dP o Gam) K
+//   dk = E beta (u dh'^T) - ga (dx h^T) + (dP o Gam)^T Q + (N + N^T) K,  N = dB o Gam
+//   dbeta_r = ddelta_r . u_r - sum_m B_mr Zu_mr
+//   X = strict_lower(dB o B + dP o P),  Y_r = E_r delta_r . (K dh')_r
+//   dG_r = ga_r q_r . (do h^T)_r - dx_r . (ga K h)_r - Y_r + sum_s X_rs - sum_m X_mr
+//   dG_L += sum Y + ga_L <h, dh'>,   dlog_g_t = sum_{r >= t} dG_r
+// A pair (r, s) enters dG_r and dG_s with the same X_rs, so that the running
+// sum cancels what does not cross t exactly; the diagonal of P, which no decay
+// touches, is left out of X for the same reason.
+#pragma once
+
+#include "gdn_train_internal.h"
+
+namespace gdn {
+namespace bwd {
+
+constexpr int C = 64;
+
+struct ChunkAt {
+    int b;          // sequence
+    int c;          // chunk within it
+    int64_t row0;   // first row of the chunk
+    int rows;       // rows of the chunk, 1..64
+    bool last;      // the sequence's last chunk
+};
+
+// Rows of sequence b: [row0, row0 + len); offsets outside [0, T] are clamped
+// into it, as in the forward pass.
+__device__ __forceinline__ void seq_rows(const int32_t* cu, int b, int T, int64_t* row0, int64_t* len)
+{
+    if (cu) {
+        const int64_t a = min(max((int64_t)cu[b], (int64_t)0), (int64_t)T);
+        const int64_t e = min(max((int64_t)cu[b + 1], a), (int64_t)T);
+        *row0 = a;
+        *len = e - a;
+    } else {
+        *row0 = (int64_t)b * T;
+        *len = T;
+    }
+}
+
+// First chunk of each sequence, base[0 .. B] (one workgroup of 256 threads).
+__device__ __forceinline__ void chunk_table(const int32_t* cu, int B, int T, int32_t* base, int32_t* part)
+{
+    const int tid = threadIdx.x;
+    const int per = (B + 255) / 256;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int32_t s = 0;
+    for (int b = b0; b < b1; ++b) {
+        int64_t r0, len;
+        seq_rows(cu, b, T, &r0, &len);
+        s += (int32_t)((len + C - 1) / C);
+    }
+    part[tid] = s;
+    __syncthreads();
+    int32_t before = 0;
+    for (int i = 0; i < tid; ++i) before += part[i];
+    if (tid == 255) base[B] = before + part[255];
+    s = before;
+    for (int b = b0; b < b1; ++b) {
+        base[b] = s;
+        int64_t r0, len;
+        seq_rows(cu, b, T, &r0, &len);
+        s += (int32_t)((len + C - 1) / C);
+    }
+}
+
+// Chunk x of the call; false beyond the last one (packed grids are sized for
+// the most chunks that B sequences of T rows can have).
+__device__ __forceinline__ bool chunk_at(int x, const int32_t* cu, const int32_t* base, int B, int T,
+                                         int nc_dense, ChunkAt* at)
+{
+    int b, c;
+    if (!cu) {
+        b = x / nc_dense;
+        c = x % nc_dense;
+    } else {
+        if (x >= base[B]) return false;
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (base[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        c = x - base[b];
+    }
+    int64_t row0, len;
+    seq_rows(cu, b, T, &row0, &len);
+    at->b = b;
+    at->c = c;
+    at->row0 = row0 + (int64_t)c * C;
+    at->rows = (int)min((int64_t)C, len - (int64_t)c * C);
+    at->last = (int64_t)(c + 1) * C >= len;
+    return true;
+}
+
+// Most chunks of a call.
+inline int64_t max_chunks(int B, int T, bool packed)
+{
+    return packed ? (int64_t)T / C + B : (int64_t)B * ((T + C - 1) / C);
+}
+
+inline size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace bwd
+}  // namespace gdn

@@ -1,0 +1,559 @@
+// Layer norm / RMS norm of the recurrence's outputs times silu of a gate,
+// forward and backward, with the reduction of the weight's and the bias's
+// gradients (include/gdn_train.h).
+//
+// One row of d values is held in the registers of TPR threads (TPR <= 64: part
+// of a wave, reduced by lane exchanges; TPR >= 256: a workgroup, reduced
+// through LDS), so each input is read once and each output written once.  The
+// statistics take two steps over the registers (mean, then the squares of the
+// differences), which loses nothing where the mean is large.  Both passes are
+// bound by HBM.
+//
+// Backward: a workgroup walks rows by grid stride and keeps its columns' sums
+// of g n and g in registers; at the end its row groups are added through LDS
+// into one partial row of the workspace, and a second kernel adds the partial
+// rows in a fixed order: no atomics, the same bits run to run.
+#include "gdn_train_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxWaves = 16;
+// threads of a workgroup whose rows take tpr threads each
+__host__ __device__ constexpr int wg_threads(int tpr) { return tpr > kThreads ? tpr : kThreads; }
+
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// ---- VEC consecutive values ------------------------------------------------
+template <int VEC> __device__ __forceinline__ void load_vec(const float* p, float* f)
+{
+    if constexpr (VEC == 8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+            f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+        }
+    } else {
+        f[0] = *p;
+    }
+}
+template <int VEC> __device__ __forceinline__ void load_vec(const uint16_t* p, float* f)
+{
+    if constexpr (VEC == 8) {
+        const u4 v = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(v[j] << 16);
+            f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+        }
+    } else {
+        f[0] = bf16_bits_to_f32(*p);
+    }
+}
+template <int VEC> __device__ __forceinline__ void load_vec(const uint8_t* p, float* f)
+{
+    if constexpr (VEC == 8) {
+        const u2 v = *reinterpret_cast<const u2*>(p);
+        ckpt_unpack4(v[0], f);
+        ckpt_unpack4(v[1], f + 4);
+    } else {
+        f[0] = ckpt_unpack1(*p);
+    }
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2v{lo, hi}, b2));
+}
+template <int VEC> __device__ __forceinline__ void store_vec(float* p, const float* f)
+{
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *p = f[0];
+    }
+}
+template <int VEC> __device__ __forceinline__ void store_vec(uint16_t* p, const float* f)
+{
+    if constexpr (VEC == 8)
+        *reinterpret_cast<u4*>(p) = u4{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]),
+                                       bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+    else
+        *p = f32_to_bf16_bits(f[0]);
+}
+
+// ---- sums over the TPR threads of a row --------------------------------------
+// slot: a different one for each reduction of a row (LDS, TPR > 64 only); two
+// reductions a row keep a slot's readers ahead of its next writers.
+template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red, int slot)
+{
+    constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) x += __shfl_xor(x, o);
+    if constexpr (TPR > 64) {
+        float* r = red + slot * kMaxWaves;
+        if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) x += r[i];
+    }
+    return x;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+struct Shape {
+    int64_t rows;
+    int H, d, ng;
+    float inv_d, eps;
+    int center;
+};
+
+__device__ __forceinline__ int64_t row_at(int64_t row, const Shape& s, int64_t stride)
+{
+    if (s.H == 1) return row * stride;
+    const uint32_t t = (uint32_t)row / (uint32_t)s.H;
+    return (int64_t)t * stride + (int64_t)((uint32_t)row - t * (uint32_t)s.H) * s.d;
+}
+
+// The row's values minus their mean (center), and 1 / sqrt(var + eps).
+template <int TPR, int NV, int VEC>
+__device__ __forceinline__ float normalise(float* x, const Shape& s, int l, float* red)
+{
+    if (s.center) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < NV * VEC; ++e) m += x[e];
+        m = row_sum<TPR>(m, red, 0) * s.inv_d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * TPR + l) * VEC < s.d)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[i * VEC + e] -= m;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < NV * VEC; ++e) q = fmaf(x[e], x[e], q);
+    q = row_sum<TPR>(q, red, 1) * s.inv_d;
+    return 1.0f / sqrtf(q + s.eps);
+}
+
+// Codes and scale byte of the VEC = 8 values of each lane, a group's 128 lying
+// in 16 consecutive lanes (or in all of a narrower row's).
+template <int TPR, int NV>
+__device__ __forceinline__ void write_codes(const float* x, uint8_t* codes, uint8_t* exps, int64_t row,
+                                            const Shape& s, int l)
+{
+    constexpr int W = TPR < 16 ? TPR : 16;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int j = (i * TPR + l) * 8;
+        const float* f = x + 8 * i;
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, ckpt_magnitude(f[e]));
+#pragma unroll
+        for (int o = W / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const int byte = ckpt_exp_byte(top);
+        const float inv = ckpt_inverse(byte);
+        if (j < s.d) {
+            *reinterpret_cast<u2*>(codes + row * s.d + j) =
+                u2{ckpt_pack4(ckpt_finite(f[0]) * inv, ckpt_finite(f[1]) * inv, ckpt_finite(f[2]) * inv,
+                              ckpt_finite(f[3]) * inv),
+                   ckpt_pack4(ckpt_finite(f[4]) * inv, ckpt_finite(f[5]) * inv, ckpt_finite(f[6]) * inv,
+                              ckpt_finite(f[7]) * inv)};
+            if ((j & (kCkptGroup - 1)) == 0) exps[row * s.ng + (j >> 7)] = (uint8_t)byte;
+        }
+    }
+}
+
+// ---- forward -----------------------------------------------------------------
+template <typename T, int TPR, int NV, int VEC>
+__global__ void __launch_bounds__(wg_threads(TPR))
+gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const float* __restrict__ w,
+                        const float* __restrict__ b, T* __restrict__ y, uint8_t* __restrict__ x_codes,
+                        uint8_t* __restrict__ x_exps, uint8_t* __restrict__ z_codes,
+                        uint8_t* __restrict__ z_exps, Shape s, int64_t x_stride, int64_t z_stride,
+                        int64_t y_stride)
+{
+    __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
+    constexpr int RPW = wg_threads(TPR) / TPR;
+    const int l = threadIdx.x % TPR;
+    int turn = 0;
+    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += (int64_t)gridDim.x * RPW) {
+        const int64_t row = base + threadIdx.x / TPR;
+        const bool live = row < s.rows;   // a dead row group still takes part in the lane exchanges
+        const T* px = x + (live ? row_at(row, s, x_stride) : 0);
+        const T* pz = z ? z + (live ? row_at(row, s, z_stride) : 0) : nullptr;
+        float xv[NV * VEC], zv[NV * VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * TPR + l) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) xv[i * VEC + e] = zv[i * VEC + e] = 0.f;
+            if (live && j < s.d) {
+                load_vec<VEC>(px + j, xv + i * VEC);
+                if (pz) load_vec<VEC>(pz + j, zv + i * VEC);
+            }
+        }
+        if constexpr (VEC == 8) {
+            if (live && x_codes) write_codes<TPR, NV>(xv, x_codes, x_exps, row, s, l);
+            if (live && z_codes) write_codes<TPR, NV>(zv, z_codes, z_exps, row, s, l);
+        }
+        // LDS slots by turns: an RMS norm's one reduction a row would let the
+        // next row's writers overtake this row's readers
+        const float r = normalise<TPR, NV, VEC>(xv, s, l, red + 2 * kMaxWaves * turn);
+        turn = TPR > 64 ? turn ^ 1 : 0;
+        if (!live) continue;
+        T* py = y + row_at(row, s, y_stride);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * TPR + l) * VEC;
+            if (j >= s.d) continue;
+            float wv[VEC], bv[VEC], o[VEC];
+            load_vec<VEC>(w + j, wv);
+            if (b) load_vec<VEC>(b + j, bv);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float a = xv[i * VEC + e] * r * wv[e];
+                if (b) a += bv[e];
+                const float zz = zv[i * VEC + e];
+                o[e] = pz ? a * (zz * sigmoid(zz)) : a;
+            }
+            store_vec<VEC>(py + j, o);
+        }
+    }
+}
+
+// ---- backward ----------------------------------------------------------------
+template <typename A, typename T, int TPR, int NV, int VEC>
+__global__ void __launch_bounds__(wg_threads(TPR))
+gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_exps,
+                         const A* __restrict__ z, const uint8_t* __restrict__ z_exps,
+                         const float* __restrict__ w, const float* __restrict__ b,
+                         const T* __restrict__ dy, T* __restrict__ dx, T* __restrict__ dz,
+                         float* __restrict__ part, Shape s, int64_t x_stride, int64_t z_stride,
+                         int64_t dy_stride, int64_t dx_stride, int64_t dz_stride)
+{
+    constexpr int RPW = wg_threads(TPR) / TPR;     // rows a workgroup takes at a time
+    constexpr int N = NV * VEC;
+    constexpr bool codes = sizeof(A) == 1;
+    __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
+    __shared__ float sums[RPW > 1 ? kThreads * N : 1];
+    const int l = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+
+    float wv[N], bv[N], dw[N], db[N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int j = (i * TPR + l) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) wv[i * VEC + e] = bv[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f;
+        if (j < s.d) {
+            load_vec<VEC>(w + j, wv + i * VEC);
+            if (b) load_vec<VEC>(b + j, bv + i * VEC);
+        }
+    }
+
+    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += (int64_t)gridDim.x * RPW) {
+        const int64_t row = base + rg;
+        const bool live = row < s.rows;
+        float xv[N], zv[N], gv[N];
+        const A* px = x + (live ? row_at(row, s, x_stride) : 0);
+        const A* pz = z ? z + (live ? row_at(row, s, z_stride) : 0) : nullptr;
+        const T* pd = dy + (live ? row_at(row, s, dy_stride) : 0);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * TPR + l) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) xv[i * VEC + e] = zv[i * VEC + e] = gv[i * VEC + e] = 0.f;
+            if (live && j < s.d) {
+                load_vec<VEC>(px + j, xv + i * VEC);
+                if (pz) load_vec<VEC>(pz + j, zv + i * VEC);
+                load_vec<VEC>(pd + j, gv + i * VEC);
+                if constexpr (codes) {
+                    const float sx = ckpt_scale(x_exps[row * s.ng + (j >> 7)]);
+                    const float sz = pz ? ckpt_scale(z_exps[row * s.ng + (j >> 7)]) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        xv[i * VEC + e] *= sx;
+                        if (pz) zv[i * VEC + e] *= sz;
+                    }
+                }
+            }
+        }
+        float r = normalise<TPR, NV, VEC>(xv, s, l, red);
+        if (!live) r = 0.f;    // a dead row adds nothing to the sums, whatever eps is
+        float dot = 0.f, sum = 0.f;
+        T* pdz = dz && live ? dz + row_at(row, s, dz_stride) : nullptr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * TPR + l) * VEC;
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int c = i * VEC + e;
+                const float n = xv[c] * r;
+                xv[c] = n;
+                if (pz) {
+                    const float zz = zv[c], sg = sigmoid(zz), d = gv[c];
+                    gv[c] = d * (zz * sg);
+                    o[e] = d * fmaf(n, wv[c], bv[c]) * (sg * (1.0f + zz * (1.0f - sg)));
+                }
+                dw[c] = fmaf(gv[c], n, dw[c]);
+                db[c] += gv[c];
+                gv[c] *= wv[c];            // dn
+                dot = fmaf(gv[c], n, dot);
+                sum += gv[c];
+            }
+            if (pdz && j < s.d) store_vec<VEC>(pdz + j, o);
+        }
+        dot = row_sum<TPR>(dot, red, 2) * s.inv_d;
+        sum = s.center ? row_sum<TPR>(sum, red, 3) * s.inv_d : 0.f;
+        if (live) {
+            T* pdx = dx + row_at(row, s, dx_stride);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * TPR + l) * VEC;
+                if (j >= s.d) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int c = i * VEC + e;
+                    o[e] = (gv[c] - fmaf(xv[c], dot, sum)) * r;
+                }
+                store_vec<VEC>(pdx + j, o);
+            }
+        }
+    }
+
+    // this workgroup's partial row of dw, then of db
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float* a = half ? db : dw;
+        if constexpr (RPW > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < N; ++c) sums[c * kThreads + threadIdx.x] = a[c];
+            __syncthreads();
+            if (rg == 0) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    float t = 0.f;
+                    for (int k = 0; k < RPW; ++k) t += sums[c * kThreads + k * TPR + l];
+                    a[c] = t;
+                }
+            }
+        }
+        if (rg == 0) {
+            float* p = part + ((int64_t)blockIdx.x * 2 + half) * s.d;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * TPR + l) * VEC;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (j + e < s.d) p[j + e] = a[i * VEC + e];
+            }
+        }
+    }
+}
+
+// Sums of the partial rows, in a fixed order: 8 columns a workgroup, 32 threads
+// a column, four partial rows in flight each.  parts == 0 writes zeros.
+__global__ void __launch_bounds__(kThreads)
+gdn_norm_weight_kernel(const float* __restrict__ part, int parts, int d, float* __restrict__ dw,
+                       float* __restrict__ db)
+{
+    __shared__ float sums[32][9];
+    const int c = threadIdx.x & 7, k = threadIdx.x >> 3;
+    const int j = blockIdx.x * 8 + c, half = blockIdx.y;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (j < d) {
+        const float* p = part + (int64_t)half * d + j;
+        int i = k;
+        for (; i + 96 < parts; i += 128)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) a[u] += p[(int64_t)(i + 32 * u) * 2 * d];
+        for (; i < parts; i += 32) a[0] += p[(int64_t)i * 2 * d];
+    }
+    sums[k][c] = (a[0] + a[1]) + (a[2] + a[3]);
+    __syncthreads();
+    if (k == 0 && j < d) {
+        float t = 0.f;
+        for (int i = 0; i < 32; ++i) t += sums[i][c];
+        (half ? db : dw)[j] = t;
+    }
+}
+
+// ---- choice --------------------------------------------------------------------
+// Threads a row takes and vectors a thread: eight values a thread while d fits
+// a wave (16 lanes hold d = 128), a workgroup beyond.
+struct Choice { int tpr, nv, vec; };
+Choice choose(int d, bool vec8)
+{
+    if (vec8) {
+        if (d <= 32) return {4, 1, 8};
+        if (d <= 64) return {8, 1, 8};
+        if (d <= 128) return {16, 1, 8};
+        if (d <= 256) return {32, 1, 8};
+        if (d <= 512) return {64, 1, 8};
+        if (d <= 2048) return {256, 1, 8};
+        if (d <= 4096) return {512, 1, 8};
+        return {1024, 1, 8};
+    }
+    if (d <= 64) return {64, 1, 1};
+    if (d <= 128) return {64, 2, 1};
+    if (d <= 256) return {64, 4, 1};
+    if (d <= 1024) return {256, 4, 1};
+    if (d <= 4096) return {1024, 4, 1};
+    return {1024, 8, 1};
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool stride8(int64_t s) { return s % 8 == 0; }
+bool forward_vec8(const NormArgs& a)
+{
+    return a.d % 8 == 0 && aligned(a.x, 16) && aligned(a.z, 16) && aligned(a.y, 16) && aligned(a.w, 16) &&
+           aligned(a.b, 16) && aligned(a.x_codes, 8) && aligned(a.z_codes, 8) && stride8(a.x_stride) &&
+           (!a.z || stride8(a.z_stride)) && stride8(a.y_stride);
+}
+bool backward_vec8(const NormArgs& a)
+{
+    return a.d % 8 == 0 && aligned(a.x, 16) && aligned(a.z, 16) && aligned(a.dy, 16) && aligned(a.dx, 16) &&
+           aligned(a.dz, 16) && aligned(a.w, 16) && aligned(a.b, 16) && stride8(a.x_stride) &&
+           (!a.z || (stride8(a.z_stride) && stride8(a.dz_stride))) && stride8(a.y_stride) &&
+           stride8(a.dx_stride);
+}
+
+// Workgroups of the backward pass, and so partial rows: enough to fill 256
+// compute units several times over, few enough that the partial rows stay
+// small next to the data.
+int backward_parts(int64_t rows, int d)
+{
+    const int most = d <= 512 ? 1024 : 512;
+    const int tpr = choose(d, true).tpr, rpw = wg_threads(tpr) / tpr;
+    const int64_t need = (rows + rpw - 1) / rpw;
+    return (int)(need < most ? need : most);
+}
+// Workgroups of the forward pass: one row a row group, more by grid stride.
+unsigned forward_grid(int64_t rows, int tpr)
+{
+    const int rpw = wg_threads(tpr) / tpr;
+    const int64_t need = (rows + rpw - 1) / rpw;
+    return (unsigned)(need < (1 << 20) ? need : (1 << 20));
+}
+
+Shape shape_of(const NormArgs& a)
+{
+    return Shape{(int64_t)a.T * a.H, a.H, a.d, (a.d + kCkptGroup - 1) / kCkptGroup, 1.0f / (float)a.d,
+                 a.eps, a.center};
+}
+
+#define GDN_NORM_CHOICES(X)                                                                  \
+    X(4, 1, 8) X(8, 1, 8) X(16, 1, 8) X(32, 1, 8) X(64, 1, 8) X(256, 1, 8) X(512, 1, 8)      \
+    X(1024, 1, 8) X(64, 1, 1) X(64, 2, 1) X(64, 4, 1) X(256, 4, 1) X(1024, 4, 1) X(1024, 8, 1)
+
+template <typename T>
+void forward_typed(const NormArgs& a, bool vec8, hipStream_t s)
+{
+    const Choice c = choose(a.d, vec8);
+    const Shape sh = shape_of(a);
+    const dim3 grid(forward_grid(sh.rows, c.tpr));
+#define GDN_RUN(TPR, NV, VEC)                                                                             \
+    if (c.tpr == TPR && c.nv == NV && c.vec == VEC)                                                       \
+        hipLaunchKernelGGL((gdn_norm_forward_kernel<T, TPR, NV, VEC>), grid, dim3(wg_threads(TPR)), 0, s,        \
+                           (const T*)a.x, (const T*)a.z, a.w, a.b, (T*)a.y, a.x_codes, a.x_exps_out,      \
+                           a.z_codes, a.z_exps_out, sh, a.x_stride, a.z_stride, a.y_stride);
+    GDN_NORM_CHOICES(GDN_RUN)
+#undef GDN_RUN
+}
+
+template <typename A, typename T>
+void backward_typed(const NormArgs& a, hipStream_t s)
+{
+    const Choice c = choose(a.d, backward_vec8(a));
+    const Shape sh = shape_of(a);
+    const dim3 grid((unsigned)backward_parts(sh.rows, a.d));
+#define GDN_RUN(TPR, NV, VEC)                                                                              \
+    if (c.tpr == TPR && c.nv == NV && c.vec == VEC)                                                        \
+        hipLaunchKernelGGL((gdn_norm_backward_kernel<A, T, TPR, NV, VEC>), grid, dim3(wg_threads(TPR)), 0, s,     \
+                           (const A*)a.x, a.x_exps, (const A*)a.z, a.z_exps, a.w, a.b, (const T*)a.dy,     \
+                           (T*)a.dx, (T*)a.dz, (float*)a.workspace, sh, a.x_stride, a.z_stride,            \
+                           a.y_stride, a.dx_stride, a.dz_stride);
+    GDN_NORM_CHOICES(GDN_RUN)
+#undef GDN_RUN
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(int T, int H, int d)
+{
+    return (size_t)backward_parts((int64_t)T * H, d) * 2 * d * sizeof(float);
+}
+
+Geometry norm_forward_geometry(const NormArgs& a)
+{
+    const Choice c = choose(a.d, forward_vec8(a));
+    return Geometry{c.vec == 8 ? "gdn_norm_forward_kernel<8>" : "gdn_norm_forward_kernel<1>",
+                    {forward_grid((int64_t)a.T * a.H, c.tpr), 1, 1}, (unsigned)wg_threads(c.tpr),
+                    c.tpr > 64 ? (unsigned)(4 * kMaxWaves * sizeof(float)) : 4u};
+}
+
+Geometry norm_backward_geometry(const NormArgs& a)
+{
+    const Choice c = choose(a.d, backward_vec8(a));
+    return Geometry{c.vec == 8 ? "gdn_norm_backward_kernel<8>+gdn_norm_weight_kernel"
+                               : "gdn_norm_backward_kernel<1>+gdn_norm_weight_kernel",
+                    {(unsigned)backward_parts((int64_t)a.T * a.H, a.d), 1, 1}, (unsigned)wg_threads(c.tpr),
+                    (unsigned)(c.tpr > 64 ? 4 * kMaxWaves * sizeof(float)
+                                          : kThreads * c.nv * c.vec * sizeof(float))};
+}
+
+hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s)
+{
+    if (a.T == 0) return hipSuccess;
+    const bool v8 = forward_vec8(a);
+    if (a.io_dtype == 0) forward_typed<float>(a, v8, s);
+    else forward_typed<uint16_t>(a, v8, s);
+    hipError_t e = hipGetLastError();
+    // value by value, the lanes of a row do not hold whole groups: the
+    // checkpoints are passes of their own
+    for (int i = 0; i < 2 && !v8 && e == hipSuccess; ++i) {
+        CkptArgs c{};
+        c.x = i ? a.z : a.x;
+        c.codes = i ? a.z_codes : a.x_codes;
+        c.exps_out = i ? a.z_exps_out : a.x_exps_out;
+        if (!c.codes) continue;
+        c.rows = (int64_t)a.T * a.H;
+        c.d = a.d;
+        c.stride = i ? a.z_stride : a.x_stride;
+        c.dtype = a.io_dtype;
+        e = launch_ckpt_store_heads(c, a.H, s);
+    }
+    return e;
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s)
+{
+    if (a.T > 0) {
+        if (a.act_dtype == 2) {
+            if (a.io_dtype == 0) backward_typed<uint8_t, float>(a, s);
+            else backward_typed<uint8_t, uint16_t>(a, s);
+        } else if (a.io_dtype == 0) {
+            backward_typed<float, float>(a, s);
+        } else {
+            backward_typed<uint16_t, uint16_t>(a, s);
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(gdn_norm_weight_kernel, dim3((a.d + 7) / 8, a.db ? 2 : 1), dim3(kThreads), 0, s,
+                       (const float*)a.workspace, a.T > 0 ? backward_parts((int64_t)a.T * a.H, a.d) : 0, a.d,
+                       a.dw, a.db);
+    return hipGetLastError();
+}
+
+}  // namespace gdn
