@@ -137,10 +137,13 @@ int gdn_norm_backward_plan(const void* x, const uint8_t* x_exps, const void* z, 
  * With GDN_BF16 the gates' gradients are rounded to bf16 too: they go into the
  * bf16 product with the gate projection's weight.
  *
- * Kernels: the generic fp32 kernels (dk, dv <= 128).
+ * Kernels: bf16 or 8-bit inputs with grad_dtype GDN_BF16, dk == dv == 128 and
+ * 16-byte aligned pointers run on bf16 MFMA (fp32 accumulation and states);
+ * everything else (dk, dv <= 128) on the generic fp32 kernels.
  * gdn_last_route() names what ran.
  * workspace: gdn_backward_workspace_bytes() bytes, asked with the same sizes,
- * types and packed = (cu_seqlens != NULL), aligned to 16 bytes.
+ * types and packed = (cu_seqlens != NULL), aligned to 16 bytes; it covers
+ * either route.
  *
  * Limits: B, Hk, Hv, dk, dv >= 1, T >= 0, B and Hv <= 65535, Hv a multiple of
  * Hk, dk, dv <= 128; any finite gates with log_g <= 0.

@@ -658,7 +658,14 @@ hipError_t launch_act(const Args& k, int grad, int64_t chunks, hipStream_t s)
 
 }  // namespace
 
-size_t backward_workspace_need(const BackwardArgs& a) { return layout(a).total; }
+size_t backward_generic_workspace_bytes(const BackwardArgs& a) { return layout(a).total; }
+
+size_t backward_workspace_need(const BackwardArgs& a)
+{
+    // the generic route's is the larger one, and an unaligned call of the MFMA
+    // route's types falls back to it
+    return backward_generic_workspace_bytes(a);
+}
 
 Geometry backward_generic_geometry(const BackwardArgs& a)
 {

@@ -1,0 +1,1010 @@
+// bf16 MFMA backward pass of the gated delta rule for dk = dv = 128 (gfx950):
+// bf16 or 8-bit q, k, v and bf16 gradients, fp32 accumulation, states in fp32.
+// The formulas are in gdn_backward_common.h.  Three kernels:
+//   prep    one workgroup per (chunk, v-head): B, P, T; W, U, Qt
+//   spine   one workgroup per (sequence, v-head, 64 dv columns, direction):
+//           the states forwards and their gradients backwards in one launch;
+//           each wave owns 16 columns, so a step's two products follow each
+//           other in its registers
+//   grads   one workgroup per (chunk, k-head): the gradients of the chunk, the
+//           v-heads of the k-head in turn, dq and dk summed in registers
+//
+// Operands.  v_mfma_f32_16x16x32_bf16: lane 16 g + n supplies A[n][8g .. 8g+7]
+// and B[8g .. 8g+7][n] of a 32-wide k-step and holds rows 4g .. 4g+3 of column
+// n.  Where an accumulator's rows become the next product's k, row m of tile t
+// stands for index sig(t, m) = 32 (t/2) + 8 (m/4) + 4 (t%2) + m%4: tiles 2j and
+// 2j+1, rounded to bf16, are then k-step j's operand as they are.
+// Every matrix in LDS is row-major bf16 in swizzled 16-byte granules; an operand
+// whose k runs along a row is one 16-byte read, one whose k runs down a column
+// two transposing reads (lane i of a group of 16 names the 8 bytes of row i/4,
+// columns 4 (i%4) .. + 3 of a 4 x 16 block and receives column i).
+#include "gdn_backward_common.h"
+
+namespace gdn {
+namespace {
+
+using bwd::C;
+using bwd::ChunkAt;
+
+constexpr int D = 128;
+constexpr int kTile = C * D * 2;        // a 64 x 128 matrix
+constexpr int kSquare = C * C * 2;      // a 64 x 64 matrix
+constexpr int kState = D * D * 2;       // a bf16 state
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef unsigned char byte;
+
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                   c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+__device__ __forceinline__ uint32_t pair(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+__device__ __forceinline__ u32x2 pack4(f32x4 a) { return u32x2{pair(a[0], a[1]), pair(a[2], a[3])}; }
+__device__ __forceinline__ u32x4 pack8(f32x4 a, f32x4 b)
+{
+    return u32x4{pair(a[0], a[1]), pair(a[2], a[3]), pair(b[0], b[1]), pair(b[2], b[3])};
+}
+__device__ __forceinline__ s16x8 frag(f32x4 a, f32x4 b) { return __builtin_bit_cast(s16x8, pack8(a, b)); }
+__device__ __forceinline__ f32x4 widen(s16x4 v)
+{
+    const u32x2 u = __builtin_bit_cast(u32x2, v);
+    return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
+                 __uint_as_float(u[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 widen_lo(s16x8 v) { return widen(s16x4{v[0], v[1], v[2], v[3]}); }
+__device__ __forceinline__ f32x4 widen_hi(s16x8 v) { return widen(s16x4{v[4], v[5], v[6], v[7]}); }
+
+// first index of tile t under sig, and sig's row for m
+__device__ __forceinline__ constexpr int sig0(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
+
+// ---- LDS matrices ------------------------------------------------------------
+// 256-byte rows (128 columns): granule q of row r at q ^ swz(r); rows r .. r + 3
+// differ in the upper two bits (a transposing read's 4 x 4 granules fall in 16
+// different places), and the 16 rows of a direct read, natural or sig, in all four.
+__device__ __forceinline__ int swz16(int r)
+{
+    return ((r & 3) << 2) | (((r >> 3) & 3) ^ (((r >> 2) & 1) << 1));
+}
+// 128-byte rows (64 columns): two rows cover the banks once.
+__device__ __forceinline__ int swz8(int r)
+{
+    return (((r >> 1) & 1) << 2) | (((r >> 3) & 1) << 1) | (((r >> 2) ^ (r >> 4)) & 1);
+}
+template <int ROW> __device__ __forceinline__ int granule(int r, int q)
+{
+    if constexpr (ROW == 256) return r * 256 + 16 * (q ^ swz16(r));
+    else return r * 128 + 16 * (q ^ swz8(r));
+}
+// eight columns of row r from granule q
+template <int ROW> __device__ __forceinline__ s16x8 row8(const byte* m, int r, int q)
+{
+    return *reinterpret_cast<const s16x8*>(m + granule<ROW>(r, q));
+}
+// rows r0 .. r0 + 3 (r0 may differ between lane groups) of this lane's column:
+// sig columns of tile t (column sig(t, n)) ...
+template <int ROW> __device__ __forceinline__ s16x4 col4_sig(const byte* m, int r0, int t)
+{
+    const int i = threadIdx.x & 15;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)(m + granule<ROW>(r0 + (i >> 2), 4 * (t >> 1) + (i & 3)) + 8 * (t & 1)));
+}
+// ... or natural ones (column 16 t + n)
+template <int ROW> __device__ __forceinline__ s16x4 col4(const byte* m, int r0, int t)
+{
+    const int i = threadIdx.x & 15;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)(m + granule<ROW>(r0 + (i >> 2), 2 * t + ((i & 3) >> 1)) + 8 * (i & 1)));
+}
+__device__ __forceinline__ s16x8 join(s16x4 a, s16x4 b)
+{
+    return s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+// k-step j (rows 32 j + 8 g .. + 7) down a column
+template <int ROW> __device__ __forceinline__ s16x8 down_sig(const byte* m, int j, int t)
+{
+    const int r = 32 * j + 8 * ((threadIdx.x & 63) >> 4);
+    return join(col4_sig<ROW>(m, r, t), col4_sig<ROW>(m, r + 4, t));
+}
+template <int ROW> __device__ __forceinline__ s16x8 down(const byte* m, int j, int t)
+{
+    const int r = 32 * j + 8 * ((threadIdx.x & 63) >> 4);
+    return join(col4<ROW>(m, r, t), col4<ROW>(m, r + 4, t));
+}
+
+// ---- global operands -----------------------------------------------------------
+// eight values (granule q) of row r of an activation of 128-wide rows
+template <typename TA> __device__ __forceinline__ u32x4 act8(const void* p, const uint8_t* exps, int64_t r, int q)
+{
+    if constexpr (sizeof(TA) == 1) {
+        const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + r * D + 8 * q);
+        const float s = ckpt_scale(exps[r]);
+        float f[8];
+        ckpt_unpack4(c[0], f);
+        ckpt_unpack4(c[1], f + 4);
+        return u32x4{pair(f[0] * s, f[1] * s), pair(f[2] * s, f[3] * s), pair(f[4] * s, f[5] * s), pair(f[6] * s, f[7] * s)};
+    } else {
+        return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + r * D + 8 * q);
+    }
+}
+
+// Workspace of one (chunk, v-head), in bytes.
+constexpr int W_W = 0;                       // [64][128]
+constexpr int W_QT = W_W + kTile;            // [64][128]
+constexpr int W_U = W_QT + kTile;            // [64][128]
+constexpr int W_TT = W_U + kTile;            // T^T [64][64]
+constexpr int W_PT = W_TT + kSquare;         // P^T [64][64]
+constexpr int W_B = W_PT + kSquare;          // B's ten lower tiles in accumulator order, 512 bytes each
+constexpr int W_P = W_B + 10 * 512;          // P's
+constexpr int W_G = W_P + 10 * 512;          // G log2(e), 64 floats; beta, 64 floats
+constexpr int W_BYTES = W_G + 512;
+
+struct Args {
+    const void *q, *k, *v, *dout;
+    const uint8_t *q_exps, *k_exps, *v_exps;
+    const float *log_g, *beta, *h0, *dht;
+    uint16_t *dq, *dk, *dv, *dg, *db;
+    float* dh0;
+    int B, T, Hk, Hv;
+    const int32_t* cu;
+    int nc_dense;
+    int32_t* base;       // chunk table (packed)
+    byte* heads;         // [chunk][Hv] W_BYTES
+    byte* h;             // [chunk][Hv] start states, bf16, transposed: [dv][dk]
+    byte* dh;            // [chunk][Hv] end gradients, likewise
+};
+
+__global__ void __launch_bounds__(256)
+gdn_bwd_table_kernel(const int32_t* __restrict__ cu, int B, int T, int32_t* __restrict__ base)
+{
+    __shared__ int32_t part[256];
+    bwd::chunk_table(cu, B, T, base, part);
+}
+
+// sum over the 16 lanes of a row of lanes
+__device__ __forceinline__ float sum16(float x)
+{
+#define GDN_ROR(n) x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 | n, 0xf, 0xf, false))
+    GDN_ROR(8); GDN_ROR(4); GDN_ROR(2); GDN_ROR(1);
+#undef GDN_ROR
+    return x;
+}
+__device__ __forceinline__ float wave_scan(float x, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const float y = __shfl_up(x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+extern __shared__ __attribute__((aligned(1024))) byte lds[];
+
+// ---- prep ------------------------------------------------------------------------
+constexpr int kBP = 68;                        // pitch of the fp32 matrix B
+constexpr int P_K = 0;                         // K
+constexpr int P_Q = P_K + kTile;               // Q, then V
+constexpr int P_B = P_Q + kTile;               // B (fp32), then T^T and (T ga)^T
+constexpr int P_BBYTES = C * kBP * 4;
+constexpr int P_D = P_B + P_BBYTES;            // T's diagonal blocks (fp32, 16 x 17 each)
+constexpr int P_TBG = P_D + 4 * 16 * 17 * 4;   // (beta T ga)^T
+constexpr int P_PT = P_TBG + kSquare;          // P^T
+constexpr int P_PTG = P_PT + kSquare;          // (P beta T ga)^T
+constexpr int P_G = P_PTG + kSquare;           // G log2(e), beta, ga, E beta
+constexpr int kPrepLds = P_G + 4 * C * 4;
+static_assert(2 * kSquare <= P_BBYTES && 2 * kPrepLds <= 160 * 1024, "two prep workgroups a compute unit");
+
+template <typename TA>
+__global__ void __launch_bounds__(256, 2)
+gdn_bwd_prep_kernel(Args a)
+{
+    ChunkAt at;
+    const int x = blockIdx.x, vh = blockIdx.y, kh = vh / (a.Hv / a.Hk);
+    if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    byte* out = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
+    byte *sK = lds + P_K, *sQ = lds + P_Q, *sTT = lds + P_B, *sTG = lds + P_B + kSquare, *sTBG = lds + P_TBG,
+         *sPT = lds + P_PT, *sPTG = lds + P_PTG;
+    float *sB = reinterpret_cast<float*>(lds + P_B), *sD = reinterpret_cast<float*>(lds + P_D),
+          *sG = reinterpret_cast<float*>(lds + P_G), *sBt = sG + C, *sGa = sBt + C, *sEb = sGa + C;
+
+    // K and Q rows to LDS, V rows to registers (rows past the chunk are zero)
+    u32x4 vr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = tid + 256 * i, r = e >> 4, q = e & 15;
+        u32x4 kv = {0, 0, 0, 0}, qv = {0, 0, 0, 0};
+        vr[i] = u32x4{0, 0, 0, 0};
+        if (r < at.rows) {
+            kv = act8<TA>(a.k, a.k_exps, (at.row0 + r) * a.Hk + kh, q);
+            qv = act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, q);
+            vr[i] = act8<TA>(a.v, a.v_exps, (at.row0 + r) * a.Hv + vh, q);
+        }
+        *reinterpret_cast<u32x4*>(sK + granule<256>(r, q)) = kv;
+        *reinterpret_cast<u32x4*>(sQ + granule<256>(r, q)) = qv;
+    }
+    if (w == 0) {
+        const bool live = lane < at.rows;
+        const int64_t r = (at.row0 + lane) * a.Hv + vh;
+        const float G = wave_scan(live ? a.log_g[r] : 0.f, lane) * kLog2e;
+        const float GL = __shfl(G, 63);
+        const float bt = live ? a.beta[r] : 0.f;
+        sG[lane] = G;
+        sBt[lane] = bt;
+        sGa[lane] = exp2f(G);
+        sEb[lane] = exp2f(GL - G) * bt;
+        float* gG = reinterpret_cast<float*>(out + W_G);
+        gG[lane] = G;
+        gG[C + lane] = bt;
+    }
+    __syncthreads();
+
+    // lower tiles: wave w forms row tile w of B and row tile 3 - w of P
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int i = half ? 3 - w : w;
+        const byte* left = half ? sQ : sK;
+        s16x8 af[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) af[ks] = row8<256>(left, 16 * i + n, 4 * ks + g);
+        const f32x4 Gr = *reinterpret_cast<const f32x4*>(sG + 16 * i + 4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 t = zero4();
+            const int c = 16 * j + n;
+            if (j <= i) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], row8<256>(sK, c, 4 * ks + g), t);
+                const float Gc = sG[c];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int r = 16 * i + 4 * g + s;
+                    t[s] = (half ? c <= r : c < r) ? t[s] * exp2f(Gr[s] - Gc) : 0.f;
+                }
+                const int tile = i * (i + 1) / 2 + j;
+                *reinterpret_cast<u32x2*>(out + (half ? W_P : W_B) + 512 * tile + 8 * lane) = pack4(t);
+            }
+            if (half)
+                *reinterpret_cast<u32x2*>(sPT + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
+            else if (j <= i)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) sB[(16 * i + 4 * g + s) * kBP + c] = t[s];
+        }
+    }
+    __syncthreads();
+    // V takes Q's place; the diagonal blocks of T = (I + B diag(beta))^-1: lane
+    // (g, n) of wave 0 forms column n of block g by forward substitution
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = tid + 256 * i;
+        *reinterpret_cast<u32x4*>(sQ + granule<256>(e >> 4, e & 15)) = vr[i];
+    }
+    if (w == 0) {
+        const float* blk = sB + (16 * g) * kBP + 16 * g;
+        float t[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) t[r] = r == n ? 1.f : 0.f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m) {
+            const float f = sBt[16 * g + m] * t[m];
+#pragma unroll
+            for (int r = m + 1; r < 16; ++r) t[r] = fmaf(-blk[r * kBP + m], f, t[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sD[(16 * g + r) * 17 + n] = t[r];
+    }
+    __syncthreads();
+    // column block w: T_iw = -T_ii sum_{m = w}^{i-1} B_im beta_m T_mw in fp32
+    // products, k of step s being 4g + s, so that an accumulator is the next
+    // product's right operand as it is
+    f32x4 Tc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Tc[i] = zero4();
+        if (i == w) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) Tc[i][s] = sD[(16 * i + 4 * g + s) * 17 + n];
+        } else if (i > w) {
+            f32x4 M = zero4();
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                if (m >= w) {
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(sB + (16 * i + n) * kBP + 16 * m + 4 * g);
+                    const f32x4 bt = *reinterpret_cast<const f32x4*>(sBt + 16 * m + 4 * g);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) M = mfma4(b[s] * bt[s], Tc[m][s], M);
+                }
+            f32x4 t = zero4();
+#pragma unroll
+            for (int s = 0; s < 4; ++s) t = mfma4(sD[(16 * i + n) * 17 + 4 * g + s], M[s], t);
+            Tc[i] = -t;
+        }
+    }
+    __syncthreads();   // every read of B is done
+    {
+        const int c = 16 * w + n;
+        const float ga = sGa[c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 bt = *reinterpret_cast<const f32x4*>(sBt + 16 * i + 4 * g);
+            const int o = granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1);
+            const u32x2 tt = pack4(Tc[i]);
+            *reinterpret_cast<u32x2*>(sTT + o) = tt;
+            *reinterpret_cast<u32x2*>(sTG + o) = pack4(Tc[i] * ga);
+            *reinterpret_cast<u32x2*>(sTBG + o) = pack4(Tc[i] * bt * ga);
+        }
+    }
+    __syncthreads();
+    // (P beta T ga)^T, row tile i of the product by wave i: A = P down P^T, B =
+    // (beta T ga)^T's rows
+    {
+        const s16x8 p0 = down<128>(sPT, 0, w), p1 = down<128>(sPT, 1, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 t = mfma(p0, row8<128>(sTBG, 16 * j + n, g), zero4());
+            t = mfma(p1, row8<128>(sTBG, 16 * j + n, 4 + g), t);
+            *reinterpret_cast<u32x2*>(sPTG + granule<128>(16 * j + n, 2 * w + (g >> 1)) + 8 * (g & 1)) = pack4(t);
+        }
+    }
+    // T^T and P^T as they are, rows in order
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = tid + 256 * i, r = e >> 3, q = e & 7;
+        *reinterpret_cast<u32x4*>(out + W_TT + 16 * e) = *reinterpret_cast<const u32x4*>(sTT + granule<128>(r, q));
+        *reinterpret_cast<u32x4*>(out + W_PT + 16 * e) = *reinterpret_cast<const u32x4*>(sPT + granule<128>(r, q));
+    }
+    __syncthreads();
+    // W, Qt and U formed transposed (dk or dv down, chunk rows across): wave w
+    // takes columns 32 w .. + 31, and each lane ends with eight consecutive
+    // columns of its row
+    s16x8 kf[2][2], vf[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            kf[i][j] = down_sig<256>(sK, j, 2 * w + i);
+            vf[i][j] = down_sig<256>(sQ, j, 2 * w + i);
+        }
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        const int r = 16 * rt + n;
+        f32x4 ww[2] = {zero4(), zero4()}, uu[2] = {zero4(), zero4()}, qq[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (2 * j > rt) continue;            // T and P are lower triangular
+            const s16x8 tg = down<128>(sTG, j, rt), tt = down<128>(sTT, j, rt), pg = down<128>(sPTG, j, rt);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ww[i] = mfma(kf[i][j], tg, ww[i]);
+                uu[i] = mfma(vf[i][j], tt, uu[i]);
+                qq[i] = mfma(kf[i][j], pg, qq[i]);
+            }
+        }
+        const float eb = sEb[r], ga = sGa[r];
+        const int o = r * 256 + 16 * (4 * w + g);
+        *reinterpret_cast<u32x4*>(out + W_W + o) = pack8(ww[0] * eb, ww[1] * eb);
+        *reinterpret_cast<u32x4*>(out + W_U + o) = pack8(uu[0] * eb, uu[1] * eb);
+        s16x8 q8 = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (r < at.rows) q8 = __builtin_bit_cast(s16x8, act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, 4 * w + g));
+        *reinterpret_cast<u32x4*>(out + W_QT + o) = pack8(widen_lo(q8) * ga - qq[0], widen_hi(q8) * ga - qq[1]);
+    }
+}
+
+// ---- spine -------------------------------------------------------------------------
+// One stage of LDS holds a chunk's matrices: forwards W, K and U's columns,
+// backwards K, W, Qt and do's columns.  The next chunk's rows wait in registers
+// and are written to the other stage while this one is read.
+constexpr int kCols = 64;
+constexpr int S_L = 0;                     // W, or K
+constexpr int S_R = S_L + kTile;           // K, or W
+constexpr int S_X = S_R + kTile;           // Qt (backwards)
+constexpr int S_C = S_X + kTile;           // U, or do: [64][64]
+constexpr int kStage = S_C + kSquare;
+constexpr int kSpineLds = 2 * kStage;
+
+template <typename TA, bool REV>
+__device__ __forceinline__ void spine_walk(const Args& a)
+{
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    const int vh = blockIdx.x >> 1, half = blockIdx.x & 1, b = blockIdx.y, kh = vh / (a.Hv / a.Hk);
+    const int col = half * kCols + 16 * w + n;       // this lane's dv column
+
+    int64_t row0, len;
+    bwd::seq_rows(a.cu, b, a.T, &row0, &len);
+    const int nc = (int)((len + C - 1) / C);
+    const int64_t x0 = a.cu ? a.base[b] : (int64_t)b * a.nc_dense;
+    const float* from = REV ? a.dht : a.h0;
+    const size_t hoff = ((size_t)b * a.Hv + vh) * D * D;
+
+    f32x4 st[8];                                     // dk index sig(t, 4g + s)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            st[t][s] = from ? from[hoff + (size_t)(sig0(t) + 8 * g + s) * D + col] : 0.f;
+
+    struct Regs {
+        u32x4 l[4], r[4], x[4], c[2];
+        float gl;
+    } in;
+    auto fetch = [&](int i) {
+        const int c = REV ? nc - 1 - i : i;
+        const byte* head = a.heads + ((size_t)(x0 + c) * a.Hv + vh) * W_BYTES;
+        const int64_t r0 = row0 + (int64_t)c * C;
+        const int rows = (int)min((int64_t)C, len - (int64_t)c * C);
+        u32x4* K = REV ? in.l : in.r;
+        u32x4* W = REV ? in.r : in.l;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = tid + 256 * j, r = e >> 4, q = e & 15;
+            W[j] = *reinterpret_cast<const u32x4*>(head + W_W + 16 * e);
+            if (REV) in.x[j] = *reinterpret_cast<const u32x4*>(head + W_QT + 16 * e);
+            K[j] = u32x4{0, 0, 0, 0};
+            if (r < rows) K[j] = act8<TA>(a.k, a.k_exps, (r0 + r) * a.Hk + kh, q);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid + 256 * j, r = e >> 3, q = e & 7;
+            in.c[j] = u32x4{0, 0, 0, 0};
+            if (!REV)
+                in.c[j] = *reinterpret_cast<const u32x4*>(head + W_U + r * 256 + 128 * half + 16 * q);
+            else if (r < rows)
+                in.c[j] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dout) +
+                                                          ((r0 + r) * a.Hv + vh) * D + kCols * half + 8 * q);
+        }
+        in.gl = reinterpret_cast<const float*>(head + W_G)[C - 1];
+    };
+    auto put = [&](byte* S) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = tid + 256 * j, o = granule<256>(e >> 4, e & 15);
+            *reinterpret_cast<u32x4*>(S + S_L + o) = in.l[j];
+            *reinterpret_cast<u32x4*>(S + S_R + o) = in.r[j];
+            if (REV) *reinterpret_cast<u32x4*>(S + S_X + o) = in.x[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid + 256 * j;
+            *reinterpret_cast<u32x4*>(S + S_C + granule<128>(e >> 3, e & 7)) = in.c[j];
+        }
+    };
+
+    float gl = 0.f;
+    if (nc > 0) {
+        fetch(0);
+        put(lds);
+        gl = exp2f(in.gl);
+        if (nc > 1) fetch(1);
+    }
+    __syncthreads();
+    for (int i = 0; i < nc; ++i) {
+        const byte* S = lds + (i & 1) * kStage;
+        float gl_next = 0.f;
+        if (i + 1 < nc) {
+            put(lds + ((i + 1) & 1) * kStage);
+            gl_next = exp2f(in.gl);
+        }
+        if (i + 2 < nc) fetch(i + 2);
+
+        const int c = REV ? nc - 1 - i : i;
+        byte* out = (REV ? a.dh : a.h) + ((size_t)(x0 + c) * a.Hv + vh) * kState + col * 256;
+        s16x8 sb[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            sb[ks] = frag(st[2 * ks], st[2 * ks + 1]);
+            *reinterpret_cast<s16x8*>(out + 16 * (4 * ks + g)) = sb[ks];
+        }
+        s16x8 db[2], ob[2];
+        f32x4 d[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            f32x4 t = zero4();
+            const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) t = mfma(row8<256>(S + S_L, r, 4 * ks + g), sb[ks], t);
+            if (REV) d[rt] = -t;
+            else d[rt] = widen(col4<128>(S + S_C, sig0(rt) + 8 * g, w)) - t;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            db[j] = frag(d[2 * j], d[2 * j + 1]);
+            if (REV) ob[j] = down<128>(S + S_C, j, w);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            st[t] *= gl;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (REV) st[t] = mfma(down_sig<256>(S + S_X, j, t), ob[j], st[t]);
+                st[t] = mfma(down_sig<256>(S + S_R, j, t), db[j], st[t]);
+            }
+        }
+        gl = gl_next;
+        __syncthreads();
+    }
+    if (REV && a.dh0)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) a.dh0[hoff + (size_t)(sig0(t) + 8 * g + s) * D + col] = st[t][s];
+}
+
+template <typename TA>
+__global__ void __launch_bounds__(256)
+gdn_bwd_spine_kernel(Args a)
+{
+    if (blockIdx.z == 0) spine_walk<TA, false>(a);
+    else spine_walk<TA, true>(a);
+}
+
+// ---- grads -------------------------------------------------------------------------
+constexpr int kGradThreads = 512;
+constexpr int G_K = 0;
+constexpr int G_Q = G_K + kTile;
+constexpr int G_DO = G_Q + kTile;
+constexpr int G_H = G_DO + kTile;          // h^T [dv][dk]
+constexpr int G_DH = G_H + kState;         // dh'^T, then N^T and (dP o Gam)^T
+constexpr int G_U = G_DH + kState;         // V, then u^T [dv][64]
+constexpr int G_X = G_U + kTile;           // T^T and P^T, then dx^T [dv][64]
+constexpr int G_S = G_X + kTile;           // small arrays
+struct Small {
+    float G[C], beta[C], ga[C], E[C];      // G in units of log2
+    float rowG[8][C], rowB[8][C];          // by wave
+    float rowX[8][C], colX[8][C], colZ[4][C];
+    float rowQ[4][C];
+    float sumY[8], hd[8];
+};
+constexpr int kGradLds = G_S + (int)sizeof(Small);
+static_assert(kGradLds <= 160 * 1024, "the grads kernel's LDS");
+
+template <typename TA>
+__global__ void __launch_bounds__(kGradThreads)
+gdn_bwd_grads_kernel(Args a)
+{
+    ChunkAt at;
+    const int x = blockIdx.x, kh = blockIdx.y, rep = a.Hv / a.Hk;
+    if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    byte *sK = lds + G_K, *sQ = lds + G_Q, *sO = lds + G_DO, *sH = lds + G_H, *sDH = lds + G_DH, *sU = lds + G_U,
+         *sX = lds + G_X, *sTT = sX, *sPT = sX + kSquare, *sV = sU, *sN = sDH, *sM = sDH + kSquare;
+    Small& sm = *reinterpret_cast<Small*>(lds + G_S);
+
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
+        u32x4 kv = {0, 0, 0, 0}, qv = {0, 0, 0, 0};
+        if (r < at.rows) {
+            kv = act8<TA>(a.k, a.k_exps, (at.row0 + r) * a.Hk + kh, q);
+            qv = act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, q);
+        }
+        *reinterpret_cast<u32x4*>(sK + granule<256>(r, q)) = kv;
+        *reinterpret_cast<u32x4*>(sQ + granule<256>(r, q)) = qv;
+    }
+    // dq and dk, transposed: dk columns 32 wc .. + 31 down, rows 32 wr + 16 i + n
+    const int wc = w & 3, wr = w >> 2;
+    f32x4 dq[2][2], dk[2][2];              // [dk tile][row tile]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) dq[i][j] = dk[i][j] = zero4();
+
+    for (int vh = kh * rep; vh < (kh + 1) * rep; ++vh) {
+        const byte* head = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
+        const byte* hT = a.h + ((size_t)x * a.Hv + vh) * kState;
+        const byte* dhT = a.dh + ((size_t)x * a.Hv + vh) * kState;
+        __syncthreads();                   // the v-head before has read the LDS
+        float hd = 0.f;                    // <h, dh'>
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
+            const u32x4 hv = *reinterpret_cast<const u32x4*>(hT + 16 * e), dv = *reinterpret_cast<const u32x4*>(dhT + 16 * e);
+            *reinterpret_cast<u32x4*>(sH + granule<256>(r, q)) = hv;
+            *reinterpret_cast<u32x4*>(sDH + granule<256>(r, q)) = dv;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                hd = fmaf(__uint_as_float(hv[j] << 16), __uint_as_float(dv[j] << 16), hd);
+                hd = fmaf(__uint_as_float(hv[j] & 0xffff0000u), __uint_as_float(dv[j] & 0xffff0000u), hd);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
+            u32x4 ov = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
+            if (r < at.rows) {
+                const int64_t row = (at.row0 + r) * a.Hv + vh;
+                ov = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dout) + row * D + 8 * q);
+                vv = act8<TA>(a.v, a.v_exps, row, q);
+            }
+            *reinterpret_cast<u32x4*>(sO + granule<256>(r, q)) = ov;
+            *reinterpret_cast<u32x4*>(sV + granule<256>(r, q)) = vv;
+        }
+        {
+            const int o = granule<128>(tid >> 3, tid & 7);
+            *reinterpret_cast<u32x4*>(sTT + o) = *reinterpret_cast<const u32x4*>(head + W_TT + 16 * tid);
+            *reinterpret_cast<u32x4*>(sPT + o) = *reinterpret_cast<const u32x4*>(head + W_PT + 16 * tid);
+        }
+        if (w == 0) {
+            const float* gG = reinterpret_cast<const float*>(head + W_G);
+            const float G = gG[lane], GL = __shfl(G, 63);
+            sm.G[lane] = G;
+            sm.beta[lane] = gG[C + lane];
+            sm.ga[lane] = exp2f(G);
+            sm.E[lane] = exp2f(GL - G);
+        }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) hd += __shfl_xor(hd, o);
+        if (lane == 0) sm.hd[w] = hd;
+        __syncthreads();
+
+        // columns 16 w .. + 15 of dv: x, u, ddelta, dx, rows under sig
+        f32x4 kh4[4], u[4], dd[4], dx[4];
+        {
+            f32x4 kd[4];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) kh4[rt] = kd[rt] = zero4();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                const s16x8 hb = row8<256>(sH, 16 * w + n, 4 * ks + g), db = row8<256>(sDH, 16 * w + n, 4 * ks + g);
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    const s16x8 kf = row8<256>(sK, sig0(rt) + 8 * (n >> 2) + (n & 3), 4 * ks + g);
+                    kh4[rt] = mfma(kf, hb, kh4[rt]);
+                    kd[rt] = mfma(kf, db, kd[rt]);
+                }
+            }
+            f32x4 xv[4];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                kh4[rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
+                xv[rt] = widen(col4<256>(sV, sig0(rt) + 8 * g, w)) - kh4[rt];
+            }
+            const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
+            const s16x8 ob[2] = {down<256>(sO, 0, w), down<256>(sO, 1, w)};
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                // u = T x (T lower triangular), P^T do (P^T upper triangular)
+                u[rt] = mfma(down_sig<128>(sTT, 0, rt), xb[0], zero4());
+                if (rt >= 2) u[rt] = mfma(down_sig<128>(sTT, 1, rt), xb[1], u[rt]);
+                const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
+                dd[rt] = mfma(row8<128>(sPT, r, 4 + g), ob[1], zero4());
+                if (rt < 2) dd[rt] = mfma(row8<128>(sPT, r, g), ob[0], dd[rt]);
+            }
+            f32x4 yv[4];
+            float sumY = 0.f;
+            f32x4 rY[4];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const int r = sig0(rt) + 8 * g;
+                const f32x4 E = *reinterpret_cast<const f32x4*>(sm.E + r), bt = *reinterpret_cast<const f32x4*>(sm.beta + r);
+                const f32x4 ek = E * kd[rt];
+                dd[rt] += ek;
+                rY[rt] = bt * u[rt] * ek;
+                yv[rt] = bt * dd[rt];
+            }
+            const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
+                dx[rt] = mfma(row8<128>(sTT, r, 4 + g), yb[1], zero4());
+                if (rt < 2) dx[rt] = mfma(row8<128>(sTT, r, g), yb[0], dx[rt]);
+            }
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                f32x4 rg, rb;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    sumY += rY[rt][s];
+                    rg[s] = sum16(-dx[rt][s] * kh4[rt][s] - rY[rt][s]);
+                    rb[s] = sum16(dd[rt][s] * u[rt][s]);
+                }
+                if (n == 0) {
+                    *reinterpret_cast<f32x4*>(&sm.rowG[w][sig0(rt) + 8 * g]) = rg;
+                    *reinterpret_cast<f32x4*>(&sm.rowB[w][sig0(rt) + 8 * g]) = rb;
+                }
+            }
+#pragma unroll
+            for (int o = 32; o; o >>= 1) sumY += __shfl_xor(sumY, o);
+            if (lane == 0) sm.sumY[w] = sumY;
+        }
+        __syncthreads();                   // V, T^T and P^T have been read
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int o = granule<128>(16 * w + n, 4 * j + g);
+            *reinterpret_cast<u32x4*>(sU + o) = pack8(u[2 * j], u[2 * j + 1]);
+            *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[2 * j], dx[2 * j + 1]);
+        }
+        __syncthreads();
+
+        // dv = dx: row tile w % 4, dv columns 64 (w / 4) .. + 63, eight at a time
+        // from transposing reads of dx^T
+        {
+            const int r = 16 * (w & 3) + n;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const s16x8 v8 = down<128>(sX, 2 * (w >> 2) + j, w & 3);
+                if (r < at.rows)
+                    *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 64 * (w >> 2) + 32 * j + 8 * g) = v8;
+            }
+        }
+        // u dh'^T, and then dh' is not needed any more
+        const int rn[2] = {32 * wr + n, 32 * wr + 16 + n};
+        const float ga_n[2] = {sm.ga[rn[0]], sm.ga[rn[1]]};
+        {
+            const float eb[2] = {sm.E[rn[0]] * sm.beta[rn[0]], sm.E[rn[1]] * sm.beta[rn[1]]};
+            f32x4 t[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) t[i][j] = zero4();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                const s16x8 b0 = down<128>(sU, ks, 2 * wr), b1 = down<128>(sU, ks, 2 * wr + 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const s16x8 af = down_sig<256>(sDH, ks, 2 * wc + i);
+                    t[i][0] = mfma(af, b0, t[i][0]);
+                    t[i][1] = mfma(af, b1, t[i][1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) dk[i][j] += t[i][j] * eb[j];
+        }
+        // do h^T and dx h^T
+        {
+            f32x4 t[2][2], y[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) t[i][j] = y[i][j] = zero4();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                const s16x8 o0 = row8<256>(sO, rn[0], 4 * ks + g), o1 = row8<256>(sO, rn[1], 4 * ks + g);
+                const s16x8 x0 = down<128>(sX, ks, 2 * wr), x1 = down<128>(sX, ks, 2 * wr + 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const s16x8 af = down_sig<256>(sH, ks, 2 * wc + i);
+                    t[i][0] = mfma(af, o0, t[i][0]);
+                    t[i][1] = mfma(af, o1, t[i][1]);
+                    y[i][0] = mfma(af, x0, y[i][0]);
+                    y[i][1] = mfma(af, x1, y[i][1]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const s16x8 q8 = row8<256>(sQ, rn[j], 4 * wc + g);
+                const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const f32x4 d = t[i][j] * ga_n[j];
+                    dq[i][j] += d;
+                    dk[i][j] -= y[i][j] * ga_n[j];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s = fmaf(d[e], i ? q1[e] : q0[e], s);
+                }
+                s += __shfl_xor(s, 16);
+                s += __shfl_xor(s, 32);
+                if (g == 0) sm.rowQ[wc][rn[j]] = s;
+            }
+        }
+        __syncthreads();                   // dh' has been read
+
+        // rows 16 i .. + 15 of Zu (waves 0-3) or do u^T (waves 4-7) on and below
+        // the diagonal: N, dP o Gam, and X's row and column sums
+        {
+            const int i = w & 3;
+            const bool isP = w >= 4;
+            s16x8 af[4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) af[ks] = isP ? row8<256>(sO, 16 * i + n, 4 * ks + g) : down<128>(sX, ks, i);
+            const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * i + 4 * g);
+            f32x4 rx = zero4();
+            byte* dst = isP ? sM : sN;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f32x4 t = zero4();
+                const int c = 16 * j + n;
+                float cx = 0.f, cz = 0.f;
+                if (j <= i) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], down<128>(sU, ks, j), t);
+                    const int tile = i * (i + 1) / 2 + j;
+                    const f32x4 bp = widen(*reinterpret_cast<const s16x4*>(head + (isP ? W_P : W_B) + 512 * tile + 8 * lane));
+                    const float bt = sm.beta[c], Gc = sm.G[c];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int r = 16 * i + 4 * g + s;
+                        const bool below = c < r;
+                        const float val = isP ? t[s] * bt : -t[s] * bt;
+                        const float X = below ? val * bp[s] : 0.f;
+                        rx[s] += X;
+                        cx += X;
+                        if (!isP) cz = fmaf(bp[s], below ? t[s] : 0.f, cz);
+                        t[s] = (isP ? c <= r : below) ? val * exp2f(Gr[s] - Gc) : 0.f;
+                    }
+                }
+                *reinterpret_cast<u32x2*>(dst + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
+                cx += __shfl_xor(cx, 16); cx += __shfl_xor(cx, 32);
+                if (g == 0) sm.colX[w][c] = cx;
+                if (!isP) {
+                    cz += __shfl_xor(cz, 16); cz += __shfl_xor(cz, 32);
+                    if (g == 0) sm.colZ[w][c] = cz;
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float v = sum16(rx[s]);
+                if (n == 0) sm.rowX[w][16 * i + 4 * g + s] = v;
+            }
+        }
+        __syncthreads();
+
+        // (dP o Gam) K to dq; (dP o Gam)^T Q + (N + N^T) K to dk
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            s16x8 kf[2], qf[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                kf[i] = down_sig<256>(sK, ks, 2 * wc + i);
+                qf[i] = down_sig<256>(sQ, ks, 2 * wc + i);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const s16x8 m0 = down<128>(sM, ks, 2 * wr + j), m1 = row8<128>(sM, rn[j], 4 * ks + g);
+                const s16x8 n0 = down<128>(sN, ks, 2 * wr + j), n1 = row8<128>(sN, rn[j], 4 * ks + g);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    dq[i][j] = mfma(kf[i], m0, dq[i][j]);
+                    dk[i][j] = mfma(qf[i], m1, dk[i][j]);
+                    dk[i][j] = mfma(kf[i], n0, dk[i][j]);
+                    dk[i][j] = mfma(kf[i], n1, dk[i][j]);
+                }
+            }
+        }
+        // the gates' gradients
+        if (w == 0) {
+            float r = 0.f, bt = 0.f, cx = 0.f, rx = 0.f, cz = 0.f, Y = 0.f, hds = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                r += sm.rowG[i][lane];
+                bt += sm.rowB[i][lane];
+                Y += sm.sumY[i];
+                hds += sm.hd[i];
+                cx += sm.colX[i][lane];
+            }
+            // row tile lane / 16 belongs to waves lane / 16 and lane / 16 + 4
+            rx = sm.rowX[lane >> 4][lane] + sm.rowX[(lane >> 4) + 4][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r += sm.rowQ[i][lane];
+                cz += sm.colZ[i][lane];
+            }
+            float d = r + (rx - cx);
+            if (lane == C - 1) d += Y + sm.ga[C - 1] * hds;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const float up = __shfl_down(d, o);
+                if (lane + o < 64) d += up;
+            }
+            if (lane < at.rows) {
+                const int64_t row = (at.row0 + lane) * a.Hv + vh;
+                a.dg[row] = f32_to_bf16_bits(d);
+                a.db[row] = f32_to_bf16_bits(bt - cz);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = 32 * wr + 16 * j + n;
+        if (r < at.rows) {
+            const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 32 * wc + 8 * g;
+            *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[0][j], dq[1][j]);
+            *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[0][j], dk[1][j]);
+        }
+    }
+}
+
+struct Layout {
+    size_t base, heads, h, dh, total;
+};
+Layout layout(int B, int T, int Hv, bool packed)
+{
+    const size_t n = (size_t)bwd::max_chunks(B, T, packed) * Hv;
+    Layout l;
+    size_t at = 0;
+    l.base = at; at += bwd::round_up(packed ? (size_t)(B + 1) * sizeof(int32_t) : 0);
+    l.heads = at; at += bwd::round_up(n * W_BYTES);
+    l.h = at; at += bwd::round_up(n * kState);
+    l.dh = at; at += bwd::round_up(n * kState);
+    l.total = at;
+    return l;
+}
+
+template <typename K>
+hipError_t allow_lds(K kernel, int bytes)
+{
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename TA>
+hipError_t launch_typed(const Args& k, int64_t chunks, hipStream_t s)
+{
+    hipError_t e;
+    if ((e = allow_lds(gdn_bwd_prep_kernel<TA>, kPrepLds)) != hipSuccess) return e;
+    if ((e = allow_lds(gdn_bwd_spine_kernel<TA>, kSpineLds)) != hipSuccess) return e;
+    if ((e = allow_lds(gdn_bwd_grads_kernel<TA>, kGradLds)) != hipSuccess) return e;
+    if (k.cu) hipLaunchKernelGGL(gdn_bwd_table_kernel, dim3(1), dim3(256), 0, s, k.cu, k.B, k.T, k.base);
+    if (chunks > 0)
+        hipLaunchKernelGGL((gdn_bwd_prep_kernel<TA>), dim3((unsigned)chunks, k.Hv), dim3(256), kPrepLds, s, k);
+    hipLaunchKernelGGL((gdn_bwd_spine_kernel<TA>), dim3(k.Hv * 2, k.B, 2), dim3(256), kSpineLds, s, k);
+    if (chunks > 0)
+        hipLaunchKernelGGL((gdn_bwd_grads_kernel<TA>), dim3((unsigned)chunks, k.Hk), dim3(kGradThreads), kGradLds, s, k);
+    return hipGetLastError();
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+const char* backward_mfma_refuses(const BackwardArgs& a)
+{
+    if (a.io_dtype == 0 || a.grad_dtype != 1) return "(generic: the MFMA route takes bf16 or 8-bit activations and bf16 gradients)";
+    if (a.dk != D || a.dv != D) return "(generic: the MFMA route takes dk = dv = 128)";
+    const size_t n = a.io_dtype == 2 ? 8 : 16;
+    if (!aligned(a.q, n) || !aligned(a.k, n) || !aligned(a.v, n) || !aligned(a.dout, 16) || !aligned(a.dq, 16) ||
+        !aligned(a.dk_out, 16) || !aligned(a.dv_out, 16))
+        return "(generic: the MFMA route takes 16-byte aligned pointers)";
+    return nullptr;
+}
+
+size_t backward_mfma_workspace_bytes(const BackwardArgs& a) { return layout(a.B, a.T, a.Hv, a.cu != nullptr).total; }
+
+Geometry backward_mfma_geometry(const BackwardArgs& a)
+{
+    return Geometry{"gdn_bwd_prep_kernel+gdn_bwd_spine_kernel+gdn_bwd_grads_kernel",
+                    {(unsigned)(a.Hv * 2), (unsigned)a.B, 2}, 256, (unsigned)kSpineLds};
+}
+
+hipError_t launch_backward_mfma(const BackwardArgs& a, hipStream_t s)
+{
+    const Layout l = layout(a.B, a.T, a.Hv, a.cu != nullptr);
+    byte* w = static_cast<byte*>(a.workspace);
+    Args k{};
+    k.q = a.q; k.k = a.k; k.v = a.v; k.dout = a.dout;
+    k.q_exps = a.q_exps; k.k_exps = a.k_exps; k.v_exps = a.v_exps;
+    k.log_g = a.log_g; k.beta = a.beta; k.h0 = a.h0; k.dht = a.dh_final;
+    k.dq = static_cast<uint16_t*>(a.dq); k.dk = static_cast<uint16_t*>(a.dk_out); k.dv = static_cast<uint16_t*>(a.dv_out);
+    k.dg = static_cast<uint16_t*>(a.dlog_g); k.db = static_cast<uint16_t*>(a.dbeta); k.dh0 = a.dh0;
+    k.B = a.B; k.T = a.T; k.Hk = a.Hk; k.Hv = a.Hv; k.cu = a.cu;
+    k.nc_dense = a.T > 0 ? (a.T + C - 1) / C : 1;
+    k.base = reinterpret_cast<int32_t*>(w + l.base);
+    k.heads = w + l.heads; k.h = w + l.h; k.dh = w + l.dh;
+    const int64_t chunks = bwd::max_chunks(a.B, a.T, a.cu != nullptr);
+    if (a.io_dtype == 1) return launch_typed<uint16_t>(k, chunks, s);
+    return launch_typed<uint8_t>(k, chunks, s);
+}
+
+}  // namespace gdn

@@ -285,7 +285,8 @@ int gdn_chunk_backward_plan(const void* q, const void* k, const void* v, const u
                                            io_dtype, grad_dtype, workspace, workspace_bytes);
     const int st = check_chunk(a);
     if (st != GDN_OK) return st;
-    gdn::route_call(gdn::backward_generic_geometry(a), "");
+    const char* why = gdn::backward_mfma_refuses(a);
+    gdn::route_call(why ? gdn::backward_generic_geometry(a) : gdn::backward_mfma_geometry(a), why ? why : "");
     return GDN_OK;
 }
 
@@ -303,7 +304,8 @@ int gdn_chunk_backward(const void* q, const void* k, const void* v, const uint8_
     const gdn::BackwardArgs a = chunk_args(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, dh_final, dq,
                                            dk_out, dv_out, dlog_g, dbeta, dh0, B, T, Hk, Hv, dk, dv, cu_seqlens,
                                            io_dtype, grad_dtype, workspace, workspace_bytes);
-    return gdn::launch_status(gdn::launch_backward_generic(a, stream));
+    return gdn::launch_status(gdn::backward_mfma_refuses(a) ? gdn::launch_backward_generic(a, stream)
+                                                            : gdn::launch_backward_mfma(a, stream));
 }
 
 }  // extern "C"
