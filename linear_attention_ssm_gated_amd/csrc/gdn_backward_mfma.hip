@@ -76,14 +76,14 @@ __device__ __forceinline__ f32x4 widen_hi(s16x8 v) { return widen(s16x4{v[4], v[
 __device__ __forceinline__ constexpr int sig0(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
 
 // ---- LDS matrices ------------------------------------------------------------
-// 256-byte rows (128 columns): granule q of row r at q ^ swz(r); rows r .. r + 3
+// 256-byte rows (128 columns): granule q of row r at q ^ swz16(r); rows r .. r + 3
 // differ in the upper two bits (a transposing read's 4 x 4 granules fall in 16
-// different places), and the 16 rows of a direct read, natural or sig, in all four.
+// different places), and the 16 rows of a direct read, natural or sig, in all
+// four.  128-byte rows (64 columns): swz8, two rows covering the banks once.
 __device__ __forceinline__ int swz16(int r)
 {
     return ((r & 3) << 2) | (((r >> 3) & 3) ^ (((r >> 2) & 1) << 1));
 }
-// 128-byte rows (64 columns): two rows cover the banks once.
 __device__ __forceinline__ int swz8(int r)
 {
     return (((r >> 1) & 1) << 2) | (((r >> 3) & 1) << 1) | (((r >> 2) ^ (r >> 4)) & 1);
@@ -93,40 +93,86 @@ template <int ROW> __device__ __forceinline__ int granule(int r, int q)
     if constexpr (ROW == 256) return r * 256 + 16 * (q ^ swz16(r));
     else return r * 128 + 16 * (q ^ swz8(r));
 }
-// eight columns of row r from granule q
-template <int ROW> __device__ __forceinline__ s16x8 row8(const byte* m, int r, int q)
+// Operand reads.  A lane's address of an operand differs from tile to tile and
+// k-step to k-step by an exclusive or of constant swizzle bits and a constant
+// offset, so that eight lane bases, one for each way of reading, serve them all.
+// fresh() keeps the compiler from forming every address ahead of a loop and
+// spilling them.
+typedef const __attribute__((address_space(3))) byte* lds_ptr;
+__device__ __forceinline__ lds_ptr at_lds(uint32_t a) { return (lds_ptr)(uintptr_t)a; }
+struct Lane {
+    uint32_t rn, rs;    // 256-byte rows: a row of 16 i + n, of sig(t, n)
+    uint32_t cs, cn;    // 256-byte rows, down a column: sig columns, natural ones
+    uint32_t hn, hs;    // 128-byte rows: rows
+    uint32_t ds, dn;    // 128-byte rows: columns
+    __device__ __forceinline__ Lane(uint32_t base)
+    {
+        const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15, kr = n >> 2, qq = n & 3;
+        const int sr = 8 * (n >> 2) + (n & 3);
+        rn = base + granule<256>(n, g);
+        rs = base + granule<256>(sr, g);
+        cs = base + granule<256>(8 * g + kr, qq);
+        cn = base + granule<256>(8 * g + kr, qq >> 1) + 8 * (qq & 1);
+        hn = base + granule<128>(n, g);
+        hs = base + granule<128>(sr, g);
+        ds = base + granule<128>(8 * g + kr, qq);
+        dn = base + granule<128>(8 * g + kr, qq >> 1) + 8 * (qq & 1);
+    }
+    __device__ __forceinline__ void fresh()
+    {
+        asm volatile("" : "+v"(rn), "+v"(rs), "+v"(cs), "+v"(cn), "+v"(hn), "+v"(hs), "+v"(ds), "+v"(dn));
+    }
+};
+__device__ __forceinline__ s16x8 rd16(uint32_t a, uint32_t off)
 {
-    return *reinterpret_cast<const s16x8*>(m + granule<ROW>(r, q));
+    return *reinterpret_cast<const __attribute__((address_space(3))) s16x8*>(at_lds(a) + off);
 }
-// rows r0 .. r0 + 3 (r0 may differ between lane groups) of this lane's column:
-// sig columns of tile t (column sig(t, n)) ...
-template <int ROW> __device__ __forceinline__ s16x4 col4_sig(const byte* m, int r0, int t)
+__device__ __forceinline__ s16x4 rdtr(uint32_t a, uint32_t off)
 {
-    const int i = threadIdx.x & 15;
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s16x4*)(m + granule<ROW>(r0 + (i >> 2), 4 * (t >> 1) + (i & 3)) + 8 * (t & 1)));
-}
-// ... or natural ones (column 16 t + n)
-template <int ROW> __device__ __forceinline__ s16x4 col4(const byte* m, int r0, int t)
-{
-    const int i = threadIdx.x & 15;
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s16x4*)(m + granule<ROW>(r0 + (i >> 2), 2 * t + ((i & 3) >> 1)) + 8 * (i & 1)));
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at_lds(a) + off));
 }
 __device__ __forceinline__ s16x8 join(s16x4 a, s16x4 b)
 {
     return s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-// k-step j (rows 32 j + 8 g .. + 7) down a column
-template <int ROW> __device__ __forceinline__ s16x8 down_sig(const byte* m, int j, int t)
+// columns 32 ks + 8 g .. + 7 of row 16 i + n, or of row sig(i, n)
+template <int ROW> __device__ __forceinline__ s16x8 row8(const Lane& l, int m, int i, int ks)
 {
-    const int r = 32 * j + 8 * ((threadIdx.x & 63) >> 4);
-    return join(col4_sig<ROW>(m, r, t), col4_sig<ROW>(m, r + 4, t));
+    if constexpr (ROW == 256) return rd16(l.rn ^ (64 * ks) ^ (32 * (i & 1)), m + 4096 * i);
+    else return rd16(l.hn ^ (64 * ks) ^ (16 * (i & 1)), m + 2048 * i);
 }
-template <int ROW> __device__ __forceinline__ s16x8 down(const byte* m, int j, int t)
+template <int ROW> __device__ __forceinline__ s16x8 row8_sig(const Lane& l, int m, int i, int ks)
 {
-    const int r = 32 * j + 8 * ((threadIdx.x & 63) >> 4);
-    return join(col4<ROW>(m, r, t), col4<ROW>(m, r + 4, t));
+    if constexpr (ROW == 256) return rd16(l.rs ^ (64 * ks) ^ (32 * (i & 1)), m + 256 * sig0(i));
+    else return rd16(l.hs ^ (64 * ks) ^ (16 * (i & 1)), m + 128 * sig0(i));
+}
+// rows 32 j + 8 g + 4 h .. + 3 of column sig(t, n), or 16 t + n
+template <int ROW> __device__ __forceinline__ s16x4 col4_sig(const Lane& l, int m, int j, int h, int t)
+{
+    if constexpr (ROW == 256) return rdtr(l.cs ^ (64 * (t >> 1)) ^ (32 * h), m + 8192 * j + 1024 * h + 8 * (t & 1));
+    else return rdtr(l.ds ^ (64 * (t >> 1)) ^ (16 * h), m + 4096 * j + 512 * h + 8 * (t & 1));
+}
+template <int ROW> __device__ __forceinline__ s16x4 col4(const Lane& l, int m, int j, int h, int t)
+{
+    if constexpr (ROW == 256) return rdtr(l.cn ^ (32 * t) ^ (32 * h), m + 8192 * j + 1024 * h);
+    else return rdtr(l.dn ^ (32 * t) ^ (16 * h), m + 4096 * j + 512 * h);
+}
+// rows 32 j + 8 g .. + 7
+template <int ROW> __device__ __forceinline__ s16x8 down_sig(const Lane& l, int m, int j, int t)
+{
+    return join(col4_sig<ROW>(l, m, j, 0, t), col4_sig<ROW>(l, m, j, 1, t));
+}
+template <int ROW> __device__ __forceinline__ s16x8 down(const Lane& l, int m, int j, int t)
+{
+    return join(col4<ROW>(l, m, j, 0, t), col4<ROW>(l, m, j, 1, t));
+}
+// A workgroup barrier that orders LDS alone: __syncthreads would also wait for
+// every global load and store in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // ---- global operands -----------------------------------------------------------
@@ -227,6 +273,8 @@ gdn_bwd_prep_kernel(Args a)
     float *sB = reinterpret_cast<float*>(lds + P_B), *sD = reinterpret_cast<float*>(lds + P_D),
           *sG = reinterpret_cast<float*>(lds + P_G), *sBt = sG + C, *sGa = sBt + C, *sEb = sGa + C;
 
+    const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
+
     // K and Q rows to LDS, V rows to registers (rows past the chunk are zero)
     u32x4 vr[4];
 #pragma unroll
@@ -256,16 +304,16 @@ gdn_bwd_prep_kernel(Args a)
         gG[lane] = G;
         gG[C + lane] = bt;
     }
-    __syncthreads();
+    lds_barrier();
 
     // lower tiles: wave w forms row tile w of B and row tile 3 - w of P
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = half ? 3 - w : w;
-        const byte* left = half ? sQ : sK;
+        const int left = half ? P_Q : P_K;
         s16x8 af[4];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) af[ks] = row8<256>(left, 16 * i + n, 4 * ks + g);
+        for (int ks = 0; ks < 4; ++ks) af[ks] = row8<256>(L, left, i, ks);
         const f32x4 Gr = *reinterpret_cast<const f32x4*>(sG + 16 * i + 4 * g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -273,7 +321,7 @@ gdn_bwd_prep_kernel(Args a)
             const int c = 16 * j + n;
             if (j <= i) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], row8<256>(sK, c, 4 * ks + g), t);
+                for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], row8<256>(L, P_K, j, ks), t);
                 const float Gc = sG[c];
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -290,7 +338,7 @@ gdn_bwd_prep_kernel(Args a)
                 for (int s = 0; s < 4; ++s) sB[(16 * i + 4 * g + s) * kBP + c] = t[s];
         }
     }
-    __syncthreads();
+    lds_barrier();
     // V takes Q's place; the diagonal blocks of T = (I + B diag(beta))^-1: lane
     // (g, n) of wave 0 forms column n of block g by forward substitution
 #pragma unroll
@@ -312,7 +360,7 @@ gdn_bwd_prep_kernel(Args a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) sD[(16 * g + r) * 17 + n] = t[r];
     }
-    __syncthreads();
+    lds_barrier();
     // column block w: T_iw = -T_ii sum_{m = w}^{i-1} B_im beta_m T_mw in fp32
     // products, k of step s being 4g + s, so that an accumulator is the next
     // product's right operand as it is
@@ -339,7 +387,7 @@ gdn_bwd_prep_kernel(Args a)
             Tc[i] = -t;
         }
     }
-    __syncthreads();   // every read of B is done
+    lds_barrier();   // every read of B is done
     {
         const int c = 16 * w + n;
         const float ga = sGa[c];
@@ -353,15 +401,15 @@ gdn_bwd_prep_kernel(Args a)
             *reinterpret_cast<u32x2*>(sTBG + o) = pack4(Tc[i] * bt * ga);
         }
     }
-    __syncthreads();
+    lds_barrier();
     // (P beta T ga)^T, row tile i of the product by wave i: A = P down P^T, B =
     // (beta T ga)^T's rows
     {
-        const s16x8 p0 = down<128>(sPT, 0, w), p1 = down<128>(sPT, 1, w);
+        const s16x8 p0 = down<128>(L, P_PT, 0, w), p1 = down<128>(L, P_PT, 1, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4 t = mfma(p0, row8<128>(sTBG, 16 * j + n, g), zero4());
-            t = mfma(p1, row8<128>(sTBG, 16 * j + n, 4 + g), t);
+            f32x4 t = mfma(p0, row8<128>(L, P_TBG, j, 0), zero4());
+            t = mfma(p1, row8<128>(L, P_TBG, j, 1), t);
             *reinterpret_cast<u32x2*>(sPTG + granule<128>(16 * j + n, 2 * w + (g >> 1)) + 8 * (g & 1)) = pack4(t);
         }
     }
@@ -372,7 +420,7 @@ gdn_bwd_prep_kernel(Args a)
         *reinterpret_cast<u32x4*>(out + W_TT + 16 * e) = *reinterpret_cast<const u32x4*>(sTT + granule<128>(r, q));
         *reinterpret_cast<u32x4*>(out + W_PT + 16 * e) = *reinterpret_cast<const u32x4*>(sPT + granule<128>(r, q));
     }
-    __syncthreads();
+    lds_barrier();
     // W, Qt and U formed transposed (dk or dv down, chunk rows across): wave w
     // takes columns 32 w .. + 31, and each lane ends with eight consecutive
     // columns of its row
@@ -381,8 +429,8 @@ gdn_bwd_prep_kernel(Args a)
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            kf[i][j] = down_sig<256>(sK, j, 2 * w + i);
-            vf[i][j] = down_sig<256>(sQ, j, 2 * w + i);
+            kf[i][j] = down_sig<256>(L, P_K, j, 2 * w + i);
+            vf[i][j] = down_sig<256>(L, P_Q, j, 2 * w + i);
         }
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
@@ -391,7 +439,7 @@ gdn_bwd_prep_kernel(Args a)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (2 * j > rt) continue;            // T and P are lower triangular
-            const s16x8 tg = down<128>(sTG, j, rt), tt = down<128>(sTT, j, rt), pg = down<128>(sPTG, j, rt);
+            const s16x8 tg = down<128>(L, P_B + kSquare, j, rt), tt = down<128>(L, P_B, j, rt), pg = down<128>(L, P_PTG, j, rt);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 ww[i] = mfma(kf[i][j], tg, ww[i]);
@@ -489,6 +537,7 @@ __device__ __forceinline__ void spine_walk(const Args& a)
         }
     };
 
+    const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
     float gl = 0.f;
     if (nc > 0) {
         fetch(0);
@@ -496,9 +545,9 @@ __device__ __forceinline__ void spine_walk(const Args& a)
         gl = exp2f(in.gl);
         if (nc > 1) fetch(1);
     }
-    __syncthreads();
+    lds_barrier();
     for (int i = 0; i < nc; ++i) {
-        const byte* S = lds + (i & 1) * kStage;
+        const int S = (i & 1) * kStage;
         float gl_next = 0.f;
         if (i + 1 < nc) {
             put(lds + ((i + 1) & 1) * kStage);
@@ -519,28 +568,27 @@ __device__ __forceinline__ void spine_walk(const Args& a)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             f32x4 t = zero4();
-            const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) t = mfma(row8<256>(S + S_L, r, 4 * ks + g), sb[ks], t);
+            for (int ks = 0; ks < 4; ++ks) t = mfma(row8_sig<256>(L, S + S_L, rt, ks), sb[ks], t);
             if (REV) d[rt] = -t;
-            else d[rt] = widen(col4<128>(S + S_C, sig0(rt) + 8 * g, w)) - t;
+            else d[rt] = widen(col4<128>(L, S + S_C, rt >> 1, rt & 1, w)) - t;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             db[j] = frag(d[2 * j], d[2 * j + 1]);
-            if (REV) ob[j] = down<128>(S + S_C, j, w);
+            if (REV) ob[j] = down<128>(L, S + S_C, j, w);
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             st[t] *= gl;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (REV) st[t] = mfma(down_sig<256>(S + S_X, j, t), ob[j], st[t]);
-                st[t] = mfma(down_sig<256>(S + S_R, j, t), db[j], st[t]);
+                if (REV) st[t] = mfma(down_sig<256>(L, S + S_X, j, t), ob[j], st[t]);
+                st[t] = mfma(down_sig<256>(L, S + S_R, j, t), db[j], st[t]);
             }
         }
         gl = gl_next;
-        __syncthreads();
+        lds_barrier();
     }
     if (REV && a.dh0)
 #pragma unroll
@@ -601,6 +649,7 @@ gdn_bwd_grads_kernel(Args a)
         *reinterpret_cast<u32x4*>(sK + granule<256>(r, q)) = kv;
         *reinterpret_cast<u32x4*>(sQ + granule<256>(r, q)) = qv;
     }
+    Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
     // dq and dk, transposed: dk columns 32 wc .. + 31 down, rows 32 wr + 16 i + n
     const int wc = w & 3, wr = w >> 2;
     f32x4 dq[2][2], dk[2][2];              // [dk tile][row tile]
@@ -613,7 +662,8 @@ gdn_bwd_grads_kernel(Args a)
         const byte* head = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
         const byte* hT = a.h + ((size_t)x * a.Hv + vh) * kState;
         const byte* dhT = a.dh + ((size_t)x * a.Hv + vh) * kState;
-        __syncthreads();                   // the v-head before has read the LDS
+        L.fresh();
+        lds_barrier();                   // the v-head before has read the LDS
         float hd = 0.f;                    // <h, dh'>
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -655,7 +705,7 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
         for (int o = 32; o; o >>= 1) hd += __shfl_xor(hd, o);
         if (lane == 0) sm.hd[w] = hd;
-        __syncthreads();
+        lds_barrier();
 
         // columns 16 w .. + 15 of dv: x, u, ddelta, dx, rows under sig
         f32x4 kh4[4], u[4], dd[4], dx[4];
@@ -665,10 +715,10 @@ gdn_bwd_grads_kernel(Args a)
             for (int rt = 0; rt < 4; ++rt) kh4[rt] = kd[rt] = zero4();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 hb = row8<256>(sH, 16 * w + n, 4 * ks + g), db = row8<256>(sDH, 16 * w + n, 4 * ks + g);
+                const s16x8 hb = row8<256>(L, G_H, w, ks), db = row8<256>(L, G_DH, w, ks);
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) {
-                    const s16x8 kf = row8<256>(sK, sig0(rt) + 8 * (n >> 2) + (n & 3), 4 * ks + g);
+                    const s16x8 kf = row8_sig<256>(L, G_K, rt, ks);
                     kh4[rt] = mfma(kf, hb, kh4[rt]);
                     kd[rt] = mfma(kf, db, kd[rt]);
                 }
@@ -677,18 +727,17 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 kh4[rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
-                xv[rt] = widen(col4<256>(sV, sig0(rt) + 8 * g, w)) - kh4[rt];
+                xv[rt] = widen(col4<256>(L, G_U, rt >> 1, rt & 1, w)) - kh4[rt];
             }
             const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
-            const s16x8 ob[2] = {down<256>(sO, 0, w), down<256>(sO, 1, w)};
+            const s16x8 ob[2] = {down<256>(L, G_DO, 0, w), down<256>(L, G_DO, 1, w)};
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 // u = T x (T lower triangular), P^T do (P^T upper triangular)
-                u[rt] = mfma(down_sig<128>(sTT, 0, rt), xb[0], zero4());
-                if (rt >= 2) u[rt] = mfma(down_sig<128>(sTT, 1, rt), xb[1], u[rt]);
-                const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
-                dd[rt] = mfma(row8<128>(sPT, r, 4 + g), ob[1], zero4());
-                if (rt < 2) dd[rt] = mfma(row8<128>(sPT, r, g), ob[0], dd[rt]);
+                u[rt] = mfma(down_sig<128>(L, G_X, 0, rt), xb[0], zero4());
+                if (rt >= 2) u[rt] = mfma(down_sig<128>(L, G_X, 1, rt), xb[1], u[rt]);
+                dd[rt] = mfma(row8_sig<128>(L, G_X + kSquare, rt, 1), ob[1], zero4());
+                if (rt < 2) dd[rt] = mfma(row8_sig<128>(L, G_X + kSquare, rt, 0), ob[0], dd[rt]);
             }
             f32x4 yv[4];
             float sumY = 0.f;
@@ -705,9 +754,8 @@ gdn_bwd_grads_kernel(Args a)
             const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                const int r = sig0(rt) + 8 * (n >> 2) + (n & 3);
-                dx[rt] = mfma(row8<128>(sTT, r, 4 + g), yb[1], zero4());
-                if (rt < 2) dx[rt] = mfma(row8<128>(sTT, r, g), yb[0], dx[rt]);
+                dx[rt] = mfma(row8_sig<128>(L, G_X, rt, 1), yb[1], zero4());
+                if (rt < 2) dx[rt] = mfma(row8_sig<128>(L, G_X, rt, 0), yb[0], dx[rt]);
             }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
@@ -727,14 +775,14 @@ gdn_bwd_grads_kernel(Args a)
             for (int o = 32; o; o >>= 1) sumY += __shfl_xor(sumY, o);
             if (lane == 0) sm.sumY[w] = sumY;
         }
-        __syncthreads();                   // V, T^T and P^T have been read
+        lds_barrier();                   // V, T^T and P^T have been read
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int o = granule<128>(16 * w + n, 4 * j + g);
             *reinterpret_cast<u32x4*>(sU + o) = pack8(u[2 * j], u[2 * j + 1]);
             *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[2 * j], dx[2 * j + 1]);
         }
-        __syncthreads();
+        lds_barrier();
 
         // dv = dx: row tile w % 4, dv columns 64 (w / 4) .. + 63, eight at a time
         // from transposing reads of dx^T
@@ -742,7 +790,7 @@ gdn_bwd_grads_kernel(Args a)
             const int r = 16 * (w & 3) + n;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 v8 = down<128>(sX, 2 * (w >> 2) + j, w & 3);
+                const s16x8 v8 = down<128>(L, G_X, 2 * (w >> 2) + j, w & 3);
                 if (r < at.rows)
                     *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 64 * (w >> 2) + 32 * j + 8 * g) = v8;
             }
@@ -759,10 +807,10 @@ gdn_bwd_grads_kernel(Args a)
                 for (int j = 0; j < 2; ++j) t[i][j] = zero4();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 b0 = down<128>(sU, ks, 2 * wr), b1 = down<128>(sU, ks, 2 * wr + 1);
+                const s16x8 b0 = down<128>(L, G_U, ks, 2 * wr), b1 = down<128>(L, G_U, ks, 2 * wr + 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const s16x8 af = down_sig<256>(sDH, ks, 2 * wc + i);
+                    const s16x8 af = down_sig<256>(L, G_DH, ks, 2 * wc + i);
                     t[i][0] = mfma(af, b0, t[i][0]);
                     t[i][1] = mfma(af, b1, t[i][1]);
                 }
@@ -781,11 +829,11 @@ gdn_bwd_grads_kernel(Args a)
                 for (int j = 0; j < 2; ++j) t[i][j] = y[i][j] = zero4();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 o0 = row8<256>(sO, rn[0], 4 * ks + g), o1 = row8<256>(sO, rn[1], 4 * ks + g);
-                const s16x8 x0 = down<128>(sX, ks, 2 * wr), x1 = down<128>(sX, ks, 2 * wr + 1);
+                const s16x8 o0 = row8<256>(L, G_DO, 2 * wr, ks), o1 = row8<256>(L, G_DO, 2 * wr + 1, ks);
+                const s16x8 x0 = down<128>(L, G_X, ks, 2 * wr), x1 = down<128>(L, G_X, ks, 2 * wr + 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const s16x8 af = down_sig<256>(sH, ks, 2 * wc + i);
+                    const s16x8 af = down_sig<256>(L, G_H, ks, 2 * wc + i);
                     t[i][0] = mfma(af, o0, t[i][0]);
                     t[i][1] = mfma(af, o1, t[i][1]);
                     y[i][0] = mfma(af, x0, y[i][0]);
@@ -794,7 +842,7 @@ gdn_bwd_grads_kernel(Args a)
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 q8 = row8<256>(sQ, rn[j], 4 * wc + g);
+                const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, wc);
                 const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
                 float s = 0.f;
 #pragma unroll
@@ -810,7 +858,7 @@ gdn_bwd_grads_kernel(Args a)
                 if (g == 0) sm.rowQ[wc][rn[j]] = s;
             }
         }
-        __syncthreads();                   // dh' has been read
+        lds_barrier();                   // dh' has been read
 
         // rows 16 i .. + 15 of Zu (waves 0-3) or do u^T (waves 4-7) on and below
         // the diagonal: N, dP o Gam, and X's row and column sums
@@ -819,7 +867,7 @@ gdn_bwd_grads_kernel(Args a)
             const bool isP = w >= 4;
             s16x8 af[4];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) af[ks] = isP ? row8<256>(sO, 16 * i + n, 4 * ks + g) : down<128>(sX, ks, i);
+            for (int ks = 0; ks < 4; ++ks) af[ks] = isP ? row8<256>(L, G_DO, i, ks) : down<128>(L, G_X, ks, i);
             const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * i + 4 * g);
             f32x4 rx = zero4();
             byte* dst = isP ? sM : sN;
@@ -830,7 +878,7 @@ gdn_bwd_grads_kernel(Args a)
                 float cx = 0.f, cz = 0.f;
                 if (j <= i) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], down<128>(sU, ks, j), t);
+                    for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], down<128>(L, G_U, ks, j), t);
                     const int tile = i * (i + 1) / 2 + j;
                     const f32x4 bp = widen(*reinterpret_cast<const s16x4*>(head + (isP ? W_P : W_B) + 512 * tile + 8 * lane));
                     const float bt = sm.beta[c], Gc = sm.G[c];
@@ -860,7 +908,7 @@ gdn_bwd_grads_kernel(Args a)
                 if (n == 0) sm.rowX[w][16 * i + 4 * g + s] = v;
             }
         }
-        __syncthreads();
+        lds_barrier();
 
         // (dP o Gam) K to dq; (dP o Gam)^T Q + (N + N^T) K to dk
 #pragma unroll
@@ -868,13 +916,13 @@ gdn_bwd_grads_kernel(Args a)
             s16x8 kf[2], qf[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                kf[i] = down_sig<256>(sK, ks, 2 * wc + i);
-                qf[i] = down_sig<256>(sQ, ks, 2 * wc + i);
+                kf[i] = down_sig<256>(L, G_K, ks, 2 * wc + i);
+                qf[i] = down_sig<256>(L, G_Q, ks, 2 * wc + i);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 m0 = down<128>(sM, ks, 2 * wr + j), m1 = row8<128>(sM, rn[j], 4 * ks + g);
-                const s16x8 n0 = down<128>(sN, ks, 2 * wr + j), n1 = row8<128>(sN, rn[j], 4 * ks + g);
+                const s16x8 m0 = down<128>(L, G_DH + kSquare, ks, 2 * wr + j), m1 = row8<128>(L, G_DH + kSquare, 2 * wr + j, ks);
+                const s16x8 n0 = down<128>(L, G_DH, ks, 2 * wr + j), n1 = row8<128>(L, G_DH, 2 * wr + j, ks);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     dq[i][j] = mfma(kf[i], m0, dq[i][j]);
