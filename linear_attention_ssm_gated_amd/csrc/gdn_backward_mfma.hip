@@ -175,21 +175,74 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Nothing is moved across: a batch of operand reads is issued whole ahead of the
+// products of the batch before, not one by one in front of each product.
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---- global operands -----------------------------------------------------------
-// eight values (granule q) of row r of an activation of 128-wide rows
-template <typename TA> __device__ __forceinline__ u32x4 act8(const void* p, const uint8_t* exps, int64_t r, int q)
+// Rows of a chunk through a buffer resource whose range ends with the chunk:
+// rows past it read as zero, without a branch.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ uint64_t uniform(uint64_t v)
 {
-    if constexpr (sizeof(TA) == 1) {
-        const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + r * D + 8 * q);
-        const float s = ckpt_scale(exps[r]);
+    // (the builtin's int must not be sign-extended into the upper half)
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+    return ((uint64_t)hi << 32) | lo;
+}
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((uint64_t)base), (short)0,
+                                             (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+}
+// Eight values of an activation as they lie in memory (bf16, or codes with the
+// row's scale byte), and as bf16: a code times a power of two is exact in bf16.
+template <typename TA> struct Raw;
+template <> struct Raw<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ u32x4 bits() const { return v; }
+};
+template <> struct Raw<uint8_t> {
+    u32x2 c;
+    uint32_t e;
+    __device__ __forceinline__ u32x4 bits() const
+    {
+        const float s = ckpt_scale((int)e);
         float f[8];
         ckpt_unpack4(c[0], f);
         ckpt_unpack4(c[1], f + 4);
         return u32x4{pair(f[0] * s, f[1] * s), pair(f[2] * s, f[3] * s), pair(f[4] * s, f[5] * s), pair(f[6] * s, f[7] * s)};
-    } else {
-        return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + r * D + 8 * q);
     }
-}
+};
+// One head's rows of a chunk of an activation [tokens][heads][128].
+template <typename TA> struct Rows {
+    rsrc_t data, exps;
+    uint32_t stride, heads;
+    __device__ __forceinline__ Rows(const void* p, const uint8_t* e, int64_t row0, int rows, int H, int head)
+    {
+        const int64_t first = row0 * H + head;
+        stride = (uint32_t)H * D * (uint32_t)sizeof(TA);
+        heads = (uint32_t)H;
+        data = make_rsrc(static_cast<const TA*>(p) + first * D, (uint32_t)rows * stride);
+        if constexpr (sizeof(TA) == 1) exps = make_rsrc(e + first, (uint32_t)rows * heads);
+    }
+    // granule q (eight values) of row r
+    __device__ __forceinline__ Raw<TA> load(int r, int q) const
+    {
+        Raw<TA> x;
+        if constexpr (sizeof(TA) == 1) {
+            x.c = __builtin_amdgcn_raw_buffer_load_b64(data, (uint32_t)r * stride + 8 * q, 0, 0);
+            x.e = __builtin_amdgcn_raw_buffer_load_b8(exps, (uint32_t)r * heads, 0, 0);
+        } else {
+            x.v = load16(data, (uint32_t)r * stride + 16 * q);
+        }
+        return x;
+    }
+};
 
 // Workspace of one (chunk, v-head), in bytes.
 constexpr int W_W = 0;                       // [64][128]
@@ -276,19 +329,28 @@ gdn_bwd_prep_kernel(Args a)
     const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
 
     // K and Q rows to LDS, V rows to registers (rows past the chunk are zero)
-    u32x4 vr[4];
+    const Rows<TA> rq(a.q, a.q_exps, at.row0, at.rows, a.Hk, kh);
+    Raw<TA> vr[4];
+    {
+        const Rows<TA> rk(a.k, a.k_exps, at.row0, at.rows, a.Hk, kh), rv(a.v, a.v_exps, at.row0, at.rows, a.Hv, vh);
+        Raw<TA> kr[4], qr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = tid + 256 * i, r = e >> 4, q = e & 15;
-        u32x4 kv = {0, 0, 0, 0}, qv = {0, 0, 0, 0};
-        vr[i] = u32x4{0, 0, 0, 0};
-        if (r < at.rows) {
-            kv = act8<TA>(a.k, a.k_exps, (at.row0 + r) * a.Hk + kh, q);
-            qv = act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, q);
-            vr[i] = act8<TA>(a.v, a.v_exps, (at.row0 + r) * a.Hv + vh, q);
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + 256 * i;
+            kr[i] = rk.load(e >> 4, e & 15);
+            qr[i] = rq.load(e >> 4, e & 15);
         }
-        *reinterpret_cast<u32x4*>(sK + granule<256>(r, q)) = kv;
-        *reinterpret_cast<u32x4*>(sQ + granule<256>(r, q)) = qv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + 256 * i;
+            vr[i] = rv.load(e >> 4, e & 15);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = tid + 256 * i, o = granule<256>(e >> 4, e & 15);
+            *reinterpret_cast<u32x4*>(sK + o) = kr[i].bits();
+            *reinterpret_cast<u32x4*>(sQ + o) = qr[i].bits();
+        }
     }
     if (w == 0) {
         const bool live = lane < at.rows;
@@ -307,35 +369,44 @@ gdn_bwd_prep_kernel(Args a)
     lds_barrier();
 
     // lower tiles: wave w forms row tile w of B and row tile 3 - w of P
+    {
+        s16x8 kf[4][4], lf[2][4];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int i = half ? 3 - w : w;
-        const int left = half ? P_Q : P_K;
-        s16x8 af[4];
+        for (int ks = 0; ks < 4; ++ks) {
+            lf[0][ks] = row8<256>(L, P_K, w, ks);
+            lf[1][ks] = row8<256>(L, P_Q, 3 - w, ks);
+        }
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) af[ks] = row8<256>(L, left, i, ks);
-        const f32x4 Gr = *reinterpret_cast<const f32x4*>(sG + 16 * i + 4 * g);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f32x4 t = zero4();
-            const int c = 16 * j + n;
-            if (j <= i) {
+            for (int ks = 0; ks < 4; ++ks) kf[j][ks] = row8<256>(L, P_K, j, ks);
+        sched_fence();
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], row8<256>(L, P_K, j, ks), t);
-                const float Gc = sG[c];
+        for (int half = 0; half < 2; ++half) {
+            const int i = half ? 3 - w : w;
+            const f32x4 Gr = *reinterpret_cast<const f32x4*>(sG + 16 * i + 4 * g);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int r = 16 * i + 4 * g + s;
-                    t[s] = (half ? c <= r : c < r) ? t[s] * exp2f(Gr[s] - Gc) : 0.f;
+            for (int j = 0; j < 4; ++j) {
+                f32x4 t = zero4();
+                const int c = 16 * j + n;
+                if (j <= i) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) t = mfma(lf[half][ks], kf[j][ks], t);
+                    const float Gc = sG[c];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int r = 16 * i + 4 * g + s;
+                        t[s] = (half ? c <= r : c < r) ? t[s] * exp2f(Gr[s] - Gc) : 0.f;
+                    }
+                    const int tile = i * (i + 1) / 2 + j;
+                    *reinterpret_cast<u32x2*>(out + (half ? W_P : W_B) + 512 * tile + 8 * lane) = pack4(t);
                 }
-                const int tile = i * (i + 1) / 2 + j;
-                *reinterpret_cast<u32x2*>(out + (half ? W_P : W_B) + 512 * tile + 8 * lane) = pack4(t);
-            }
-            if (half)
-                *reinterpret_cast<u32x2*>(sPT + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
-            else if (j <= i)
+                if (half)
+                    *reinterpret_cast<u32x2*>(sPT + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
+                else if (j <= i)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) sB[(16 * i + 4 * g + s) * kBP + c] = t[s];
+                    for (int s = 0; s < 4; ++s) sB[(16 * i + 4 * g + s) * kBP + c] = t[s];
+            }
         }
     }
     lds_barrier();
@@ -344,18 +415,27 @@ gdn_bwd_prep_kernel(Args a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = tid + 256 * i;
-        *reinterpret_cast<u32x4*>(sQ + granule<256>(e >> 4, e & 15)) = vr[i];
+        *reinterpret_cast<u32x4*>(sQ + granule<256>(e >> 4, e & 15)) = vr[i].bits();
     }
     if (w == 0) {
         const float* blk = sB + (16 * g) * kBP + 16 * g;
+        f32x4 br[16][4], bt[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) bt[m] = *reinterpret_cast<const f32x4*>(sBt + 16 * g + 4 * m);
+#pragma unroll
+        for (int r = 1; r < 16; ++r)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (4 * m < r) br[r][m] = *reinterpret_cast<const f32x4*>(blk + r * kBP + 4 * m);
+        sched_fence();
         float t[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) t[r] = r == n ? 1.f : 0.f;
 #pragma unroll
         for (int m = 0; m < 15; ++m) {
-            const float f = sBt[16 * g + m] * t[m];
+            const float f = bt[m >> 2][m & 3] * t[m];
 #pragma unroll
-            for (int r = m + 1; r < 16; ++r) t[r] = fmaf(-blk[r * kBP + m], f, t[r]);
+            for (int r = m + 1; r < 16; ++r) t[r] = fmaf(-br[r][m >> 2][m & 3], f, t[r]);
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) sD[(16 * g + r) * 17 + n] = t[r];
@@ -432,28 +512,42 @@ gdn_bwd_prep_kernel(Args a)
             kf[i][j] = down_sig<256>(L, P_K, j, 2 * w + i);
             vf[i][j] = down_sig<256>(L, P_Q, j, 2 * w + i);
         }
+    Raw<TA> q8[4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) q8[rt] = rq.load(16 * rt + n, 4 * w + g);
+    s16x8 tg[2][2], tt[2][2], pg[2][2];        // by turns: row tile rt, k-step
+    auto read = [&](int rt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (2 * j <= rt) {                  // T and P are lower triangular
+                tg[rt & 1][j] = down<128>(L, P_B + kSquare, j, rt);
+                tt[rt & 1][j] = down<128>(L, P_B, j, rt);
+                pg[rt & 1][j] = down<128>(L, P_PTG, j, rt);
+            }
+    };
+    read(0);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
+        if (rt < 3) read(rt + 1);
+        sched_fence();
         const int r = 16 * rt + n;
         f32x4 ww[2] = {zero4(), zero4()}, uu[2] = {zero4(), zero4()}, qq[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (2 * j > rt) continue;            // T and P are lower triangular
-            const s16x8 tg = down<128>(L, P_B + kSquare, j, rt), tt = down<128>(L, P_B, j, rt), pg = down<128>(L, P_PTG, j, rt);
+        for (int j = 0; j < 2; ++j)
+            if (2 * j <= rt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ww[i] = mfma(kf[i][j], tg, ww[i]);
-                uu[i] = mfma(vf[i][j], tt, uu[i]);
-                qq[i] = mfma(kf[i][j], pg, qq[i]);
-            }
-        }
+                for (int i = 0; i < 2; ++i) {
+                    ww[i] = mfma(kf[i][j], tg[rt & 1][j], ww[i]);
+                    uu[i] = mfma(vf[i][j], tt[rt & 1][j], uu[i]);
+                    qq[i] = mfma(kf[i][j], pg[rt & 1][j], qq[i]);
+                }
         const float eb = sEb[r], ga = sGa[r];
         const int o = r * 256 + 16 * (4 * w + g);
         *reinterpret_cast<u32x4*>(out + W_W + o) = pack8(ww[0] * eb, ww[1] * eb);
         *reinterpret_cast<u32x4*>(out + W_U + o) = pack8(uu[0] * eb, uu[1] * eb);
-        s16x8 q8 = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (r < at.rows) q8 = __builtin_bit_cast(s16x8, act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, 4 * w + g));
-        *reinterpret_cast<u32x4*>(out + W_QT + o) = pack8(widen_lo(q8) * ga - qq[0], widen_hi(q8) * ga - qq[1]);
+        const s16x8 qb = __builtin_bit_cast(s16x8, q8[rt].bits());
+        *reinterpret_cast<u32x4*>(out + W_QT + o) = pack8(widen_lo(qb) * ga - qq[0], widen_hi(qb) * ga - qq[1]);
+        sched_fence();
     }
 }
 
@@ -466,7 +560,8 @@ constexpr int S_L = 0;                     // W, or K
 constexpr int S_R = S_L + kTile;           // K, or W
 constexpr int S_X = S_R + kTile;           // Qt (backwards)
 constexpr int S_C = S_X + kTile;           // U, or do: [64][64]
-constexpr int kStage = S_C + kSquare;
+constexpr int S_G = S_C + kSquare;          // G_L log2(e)
+constexpr int kStage = S_G + 1024;
 constexpr int kSpineLds = 2 * kStage;
 
 template <typename TA, bool REV>
@@ -491,43 +586,40 @@ __device__ __forceinline__ void spine_walk(const Args& a)
         for (int s = 0; s < 4; ++s)
             st[t][s] = from ? from[hoff + (size_t)(sig0(t) + 8 * g + s) * D + col] : 0.f;
 
+    // a chunk's matrices on their way to LDS
     struct Regs {
-        u32x4 l[4], r[4], x[4], c[2];
+        u32x4 W[4], x[4], c[2];
+        Raw<TA> K[4];
         float gl;
-    } in;
-    auto fetch = [&](int i) {
+    } in0, in1;
+    auto fetch = [&](Regs& in, int i) {      // the i-th chunk of the walk
         const int c = REV ? nc - 1 - i : i;
         const byte* head = a.heads + ((size_t)(x0 + c) * a.Hv + vh) * W_BYTES;
         const int64_t r0 = row0 + (int64_t)c * C;
         const int rows = (int)min((int64_t)C, len - (int64_t)c * C);
-        u32x4* K = REV ? in.l : in.r;
-        u32x4* W = REV ? in.r : in.l;
+        const Rows<TA> rk(a.k, a.k_exps, r0, rows, a.Hk, kh);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = tid + 256 * j, r = e >> 4, q = e & 15;
-            W[j] = *reinterpret_cast<const u32x4*>(head + W_W + 16 * e);
+            const int e = tid + 256 * j;
+            in.W[j] = *reinterpret_cast<const u32x4*>(head + W_W + 16 * e);
             if (REV) in.x[j] = *reinterpret_cast<const u32x4*>(head + W_QT + 16 * e);
-            K[j] = u32x4{0, 0, 0, 0};
-            if (r < rows) K[j] = act8<TA>(a.k, a.k_exps, (r0 + r) * a.Hk + kh, q);
+            in.K[j] = rk.load(e >> 4, e & 15);
         }
+        const Rows<uint16_t> ro(a.dout, nullptr, r0, REV ? rows : 0, a.Hv, vh);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int e = tid + 256 * j, r = e >> 3, q = e & 7;
-            in.c[j] = u32x4{0, 0, 0, 0};
-            if (!REV)
-                in.c[j] = *reinterpret_cast<const u32x4*>(head + W_U + r * 256 + 128 * half + 16 * q);
-            else if (r < rows)
-                in.c[j] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dout) +
-                                                          ((r0 + r) * a.Hv + vh) * D + kCols * half + 8 * q);
+            in.c[j] = REV ? ro.load(r, 8 * half + q).v
+                          : *reinterpret_cast<const u32x4*>(head + W_U + r * 256 + 128 * half + 16 * q);
         }
         in.gl = reinterpret_cast<const float*>(head + W_G)[C - 1];
     };
-    auto put = [&](byte* S) {
+    auto put = [&](const Regs& in, byte* S) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int e = tid + 256 * j, o = granule<256>(e >> 4, e & 15);
-            *reinterpret_cast<u32x4*>(S + S_L + o) = in.l[j];
-            *reinterpret_cast<u32x4*>(S + S_R + o) = in.r[j];
+            *reinterpret_cast<u32x4*>(S + (REV ? S_R : S_L) + o) = in.W[j];
+            *reinterpret_cast<u32x4*>(S + (REV ? S_L : S_R) + o) = in.K[j].bits();
             if (REV) *reinterpret_cast<u32x4*>(S + S_X + o) = in.x[j];
         }
 #pragma unroll
@@ -535,25 +627,35 @@ __device__ __forceinline__ void spine_walk(const Args& a)
             const int e = tid + 256 * j;
             *reinterpret_cast<u32x4*>(S + S_C + granule<128>(e >> 3, e & 7)) = in.c[j];
         }
+        if (tid == 0) *reinterpret_cast<float*>(S + S_G) = in.gl;
     };
 
     const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
-    float gl = 0.f;
     if (nc > 0) {
-        fetch(0);
-        put(lds);
-        gl = exp2f(in.gl);
-        if (nc > 1) fetch(1);
+        fetch(in0, 0);
+        fetch(in1, min(1, nc - 1));
+        put(in0, lds);
     }
+    // the start state has arrived: else the loop's waits, which serve its first
+    // pass too, would wait for every load in flight each time
+#pragma unroll
+    for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(st[t]));
+    if (nc > 0) fetch(in0, min(2, nc - 1));
     lds_barrier();
-    for (int i = 0; i < nc; ++i) {
+    // Step i reads chunk i from stage i % 2, then writes chunk i + 1 to the other
+    // one and fetches chunk i + 3 into the registers that this leaves free: a
+    // load has two steps to arrive.  Past the end the last chunk is fetched again
+    // and written to a stage that nobody reads (no branches).
+    auto step = [&](int i, Regs& in) {
         const int S = (i & 1) * kStage;
-        float gl_next = 0.f;
-        if (i + 1 < nc) {
-            put(lds + ((i + 1) & 1) * kStage);
-            gl_next = exp2f(in.gl);
-        }
-        if (i + 2 < nc) fetch(i + 2);
+        s16x8 lf[4][4], rf[8][2], xf[8][2], ob[2];
+        s16x4 uf[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) lf[rt][ks] = row8_sig<256>(L, S + S_L, rt, ks);
+        const float gl = exp2f(*reinterpret_cast<const float*>(lds + S + S_G));
+        sched_fence();
 
         const int c = REV ? nc - 1 - i : i;
         byte* out = (REV ? a.dh : a.h) + ((size_t)(x0 + c) * a.Hv + vh) * kState + col * 256;
@@ -563,32 +665,54 @@ __device__ __forceinline__ void spine_walk(const Args& a)
             sb[ks] = frag(st[2 * ks], st[2 * ks + 1]);
             *reinterpret_cast<s16x8*>(out + 16 * (4 * ks + g)) = sb[ks];
         }
-        s16x8 db[2], ob[2];
         f32x4 d[4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            f32x4 t = zero4();
+        for (int rt = 0; rt < 4; ++rt) d[rt] = zero4();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) t = mfma(row8_sig<256>(L, S + S_L, rt, ks), sb[ks], t);
-            if (REV) d[rt] = -t;
-            else d[rt] = widen(col4<128>(L, S + S_C, rt >> 1, rt & 1, w)) - t;
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) d[rt] = mfma(lf[rt][ks], sb[ks], d[rt]);
+        // the operands of the second product, while the first one runs
+        if (!REV) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) uf[rt] = col4<128>(L, S + S_C, rt >> 1, rt & 1, w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) ob[j] = down<128>(L, S + S_C, j, w);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            db[j] = frag(d[2 * j], d[2 * j + 1]);
-            if (REV) ob[j] = down<128>(L, S + S_C, j, w);
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            st[t] *= gl;
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (REV) st[t] = mfma(down_sig<256>(L, S + S_X, j, t), ob[j], st[t]);
-                st[t] = mfma(down_sig<256>(L, S + S_R, j, t), db[j], st[t]);
+                if (REV) xf[t][j] = down_sig<256>(L, S + S_X, j, t);
+                rf[t][j] = down_sig<256>(L, S + S_R, j, t);
             }
+        sched_fence();
+#pragma unroll
+        for (int t = 0; t < 8; ++t) st[t] *= gl;
+        if (REV) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int t = 0; t < 8; ++t) st[t] = mfma(xf[t][j], ob[j], st[t]);
         }
-        gl = gl_next;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) d[rt] = REV ? -d[rt] : widen(uf[rt]) - d[rt];
+        const s16x8 db[2] = {frag(d[0], d[1]), frag(d[2], d[3])};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) st[t] = mfma(rf[t][j], db[j], st[t]);
+        sched_fence();
+        put(in, lds + (kStage - S));
+        sched_fence();
+        fetch(in, min(i + 3, nc - 1));
+        sched_fence();
         lds_barrier();
+    };
+    for (int i = 0; i < nc; i += 2) {
+        step(i, in1);
+        if (i + 1 < nc) step(i + 1, in0);
     }
     if (REV && a.dh0)
 #pragma unroll
@@ -598,7 +722,7 @@ __device__ __forceinline__ void spine_walk(const Args& a)
 }
 
 template <typename TA>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 1)
 gdn_bwd_spine_kernel(Args a)
 {
     if (blockIdx.z == 0) spine_walk<TA, false>(a);
@@ -638,16 +762,56 @@ gdn_bwd_grads_kernel(Args a)
          *sX = lds + G_X, *sTT = sX, *sPT = sX + kSquare, *sV = sU, *sN = sDH, *sM = sDH + kSquare;
     Small& sm = *reinterpret_cast<Small*>(lds + G_S);
 
+    // a v-head's matrices on their way to LDS
+    struct Regs {
+        u32x4 h[4], dh[4], o[2], tt, pt;
+        Raw<TA> v[2];
+        s16x4 bp[4];
+        float G, beta;
+    } in;
+    auto fetch = [&](int vh) {
+        const byte* head = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
+        const byte* hT = a.h + ((size_t)x * a.Hv + vh) * kState;
+        const byte* dhT = a.dh + ((size_t)x * a.Hv + vh) * kState;
+        const Rows<TA> rv(a.v, a.v_exps, at.row0, at.rows, a.Hv, vh);
+        const Rows<uint16_t> ro(a.dout, nullptr, at.row0, at.rows, a.Hv, vh);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
-        u32x4 kv = {0, 0, 0, 0}, qv = {0, 0, 0, 0};
-        if (r < at.rows) {
-            kv = act8<TA>(a.k, a.k_exps, (at.row0 + r) * a.Hk + kh, q);
-            qv = act8<TA>(a.q, a.q_exps, (at.row0 + r) * a.Hk + kh, q);
+        for (int i = 0; i < 4; ++i) {
+            in.h[i] = *reinterpret_cast<const u32x4*>(hT + 16 * (tid + kGradThreads * i));
+            in.dh[i] = *reinterpret_cast<const u32x4*>(dhT + 16 * (tid + kGradThreads * i));
         }
-        *reinterpret_cast<u32x4*>(sK + granule<256>(r, q)) = kv;
-        *reinterpret_cast<u32x4*>(sQ + granule<256>(r, q)) = qv;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + kGradThreads * i;
+            in.v[i] = rv.load(e >> 4, e & 15);
+            in.o[i] = ro.load(e >> 4, e & 15).v;
+        }
+        in.tt = *reinterpret_cast<const u32x4*>(head + W_TT + 16 * tid);
+        in.pt = *reinterpret_cast<const u32x4*>(head + W_PT + 16 * tid);
+        // B's or P's tiles of this wave's block row
+        const int i = w & 3;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            in.bp[j] = *reinterpret_cast<const s16x4*>(head + (w >= 4 ? W_P : W_B) + 512 * (i * (i + 1) / 2 + min(i, j)) + 8 * lane);
+        in.G = reinterpret_cast<const float*>(head + W_G)[lane];
+        in.beta = reinterpret_cast<const float*>(head + W_G)[C + lane];
+    };
+    {
+        const Rows<TA> rk(a.k, a.k_exps, at.row0, at.rows, a.Hk, kh), rq(a.q, a.q_exps, at.row0, at.rows, a.Hk, kh);
+        Raw<TA> kr[2], qr[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + kGradThreads * i;
+            kr[i] = rk.load(e >> 4, e & 15);
+            qr[i] = rq.load(e >> 4, e & 15);
+        }
+        fetch(kh * rep);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+            *reinterpret_cast<u32x4*>(sK + o) = kr[i].bits();
+            *reinterpret_cast<u32x4*>(sQ + o) = qr[i].bits();
+        }
     }
     Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
     // dq and dk, transposed: dk columns 32 wc .. + 31 down, rows 32 wr + 16 i + n
@@ -659,48 +823,40 @@ gdn_bwd_grads_kernel(Args a)
         for (int j = 0; j < 2; ++j) dq[i][j] = dk[i][j] = zero4();
 
     for (int vh = kh * rep; vh < (kh + 1) * rep; ++vh) {
-        const byte* head = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
-        const byte* hT = a.h + ((size_t)x * a.Hv + vh) * kState;
-        const byte* dhT = a.dh + ((size_t)x * a.Hv + vh) * kState;
         L.fresh();
-        lds_barrier();                   // the v-head before has read the LDS
+        lds_barrier();                     // the v-head before has read the LDS
         float hd = 0.f;                    // <h, dh'>
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
-            const u32x4 hv = *reinterpret_cast<const u32x4*>(hT + 16 * e), dv = *reinterpret_cast<const u32x4*>(dhT + 16 * e);
-            *reinterpret_cast<u32x4*>(sH + granule<256>(r, q)) = hv;
-            *reinterpret_cast<u32x4*>(sDH + granule<256>(r, q)) = dv;
+            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+            *reinterpret_cast<u32x4*>(sH + o) = in.h[i];
+            *reinterpret_cast<u32x4*>(sDH + o) = in.dh[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                hd = fmaf(__uint_as_float(hv[j] << 16), __uint_as_float(dv[j] << 16), hd);
-                hd = fmaf(__uint_as_float(hv[j] & 0xffff0000u), __uint_as_float(dv[j] & 0xffff0000u), hd);
+                hd = fmaf(__uint_as_float(in.h[i][j] << 16), __uint_as_float(in.dh[i][j] << 16), hd);
+                hd = fmaf(__uint_as_float(in.h[i][j] & 0xffff0000u), __uint_as_float(in.dh[i][j] & 0xffff0000u), hd);
             }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int e = tid + kGradThreads * i, r = e >> 4, q = e & 15;
-            u32x4 ov = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
-            if (r < at.rows) {
-                const int64_t row = (at.row0 + r) * a.Hv + vh;
-                ov = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dout) + row * D + 8 * q);
-                vv = act8<TA>(a.v, a.v_exps, row, q);
-            }
-            *reinterpret_cast<u32x4*>(sO + granule<256>(r, q)) = ov;
-            *reinterpret_cast<u32x4*>(sV + granule<256>(r, q)) = vv;
+            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+            *reinterpret_cast<u32x4*>(sO + o) = in.o[i];
+            *reinterpret_cast<u32x4*>(sV + o) = in.v[i].bits();
         }
         {
             const int o = granule<128>(tid >> 3, tid & 7);
-            *reinterpret_cast<u32x4*>(sTT + o) = *reinterpret_cast<const u32x4*>(head + W_TT + 16 * tid);
-            *reinterpret_cast<u32x4*>(sPT + o) = *reinterpret_cast<const u32x4*>(head + W_PT + 16 * tid);
+            *reinterpret_cast<u32x4*>(sTT + o) = in.tt;
+            *reinterpret_cast<u32x4*>(sPT + o) = in.pt;
         }
+        s16x4 bpv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bpv[j] = in.bp[j];
         if (w == 0) {
-            const float* gG = reinterpret_cast<const float*>(head + W_G);
-            const float G = gG[lane], GL = __shfl(G, 63);
-            sm.G[lane] = G;
-            sm.beta[lane] = gG[C + lane];
-            sm.ga[lane] = exp2f(G);
-            sm.E[lane] = exp2f(GL - G);
+            const float GL = __shfl(in.G, 63);
+            sm.G[lane] = in.G;
+            sm.beta[lane] = in.beta;
+            sm.ga[lane] = exp2f(in.G);
+            sm.E[lane] = exp2f(GL - in.G);
         }
 #pragma unroll
         for (int o = 32; o; o >>= 1) hd += __shfl_xor(hd, o);
@@ -784,6 +940,7 @@ gdn_bwd_grads_kernel(Args a)
         }
         lds_barrier();
 
+        fetch(min(vh + 1, (kh + 1) * rep - 1));   // the next v-head's, while this one is worked on
         // dv = dx: row tile w % 4, dv columns 64 (w / 4) .. + 63, eight at a time
         // from transposing reads of dx^T
         {
@@ -879,8 +1036,7 @@ gdn_bwd_grads_kernel(Args a)
                 if (j <= i) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], down<128>(L, G_U, ks, j), t);
-                    const int tile = i * (i + 1) / 2 + j;
-                    const f32x4 bp = widen(*reinterpret_cast<const s16x4*>(head + (isP ? W_P : W_B) + 512 * tile + 8 * lane));
+                    const f32x4 bp = widen(bpv[j]);
                     const float bt = sm.beta[c], Gc = sm.G[c];
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
