@@ -93,6 +93,12 @@ template <int ROW> __device__ __forceinline__ int granule(int r, int q)
     if constexpr (ROW == 256) return r * 256 + 16 * (q ^ swz16(r));
     else return r * 128 + 16 * (q ^ swz8(r));
 }
+// The i-th 16-byte granule of thread tid (of 256) of a matrix in row order.
+template <int ROW> __device__ __forceinline__ int staged(int tid, int i)
+{
+    if constexpr (ROW == 256) return (granule<256>(tid >> 4, tid & 15) ^ (32 * (i & 1))) + 4096 * i;
+    else return granule<128>(tid >> 3, tid & 7) + 4096 * i;
+}
 // Operand reads.  A lane's address of an operand differs from tile to tile and
 // k-step to k-step by an exclusive or of constant swizzle bits and a constant
 // offset, so that eight lane bases, one for each way of reading, serve them all.
@@ -195,9 +201,11 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes)
     return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((uint64_t)base), (short)0,
                                              (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
-__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off)
+// soff: a wave-uniform offset in an SGPR, so that a thread's loads share one
+// address register
+__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff)
 {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
 }
 // Eight values of an activation as they lie in memory (bf16, or codes with the
 // row's scale byte), and as bf16: a code times a power of two is exact in bf16.
@@ -230,15 +238,15 @@ template <typename TA> struct Rows {
         data = make_rsrc(static_cast<const TA*>(p) + first * D, (uint32_t)rows * stride);
         if constexpr (sizeof(TA) == 1) exps = make_rsrc(e + first, (uint32_t)rows * heads);
     }
-    // granule q (eight values) of row r
-    __device__ __forceinline__ Raw<TA> load(int r, int q) const
+    // granule q (eight values) of row r + dr, dr wave-uniform
+    __device__ __forceinline__ Raw<TA> load(int r, int q, int dr = 0) const
     {
         Raw<TA> x;
         if constexpr (sizeof(TA) == 1) {
-            x.c = __builtin_amdgcn_raw_buffer_load_b64(data, (uint32_t)r * stride + 8 * q, 0, 0);
-            x.e = __builtin_amdgcn_raw_buffer_load_b8(exps, (uint32_t)r * heads, 0, 0);
+            x.c = __builtin_amdgcn_raw_buffer_load_b64(data, (uint32_t)r * stride + 8 * q, (uint32_t)dr * stride, 0);
+            x.e = __builtin_amdgcn_raw_buffer_load_b8(exps, (uint32_t)r * heads, (uint32_t)dr * heads, 0);
         } else {
-            x.v = load16(data, (uint32_t)r * stride + 16 * q);
+            x.v = load16(data, (uint32_t)r * stride + 16 * q, (uint32_t)dr * stride);
         }
         return x;
     }
@@ -336,18 +344,14 @@ gdn_bwd_prep_kernel(Args a)
         Raw<TA> kr[4], qr[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i;
-            kr[i] = rk.load(e >> 4, e & 15);
-            qr[i] = rq.load(e >> 4, e & 15);
+            kr[i] = rk.load(tid >> 4, tid & 15, 16 * i);
+            qr[i] = rq.load(tid >> 4, tid & 15, 16 * i);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i;
-            vr[i] = rv.load(e >> 4, e & 15);
-        }
+        for (int i = 0; i < 4; ++i) vr[i] = rv.load(tid >> 4, tid & 15, 16 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = tid + 256 * i, o = granule<256>(e >> 4, e & 15);
+            const int o = staged<256>(tid, i);
             *reinterpret_cast<u32x4*>(sK + o) = kr[i].bits();
             *reinterpret_cast<u32x4*>(sQ + o) = qr[i].bits();
         }
@@ -414,8 +418,7 @@ gdn_bwd_prep_kernel(Args a)
     // (g, n) of wave 0 forms column n of block g by forward substitution
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int e = tid + 256 * i;
-        *reinterpret_cast<u32x4*>(sQ + granule<256>(e >> 4, e & 15)) = vr[i].bits();
+        *reinterpret_cast<u32x4*>(sQ + staged<256>(tid, i)) = vr[i].bits();
     }
     if (w == 0) {
         const float* blk = sB + (16 * g) * kBP + 16 * g;
@@ -598,34 +601,33 @@ __device__ __forceinline__ void spine_walk(const Args& a)
         const int64_t r0 = row0 + (int64_t)c * C;
         const int rows = (int)min((int64_t)C, len - (int64_t)c * C);
         const Rows<TA> rk(a.k, a.k_exps, r0, rows, a.Hk, kh);
+        const rsrc_t rh = make_rsrc(head, W_BYTES);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = tid + 256 * j;
-            in.W[j] = *reinterpret_cast<const u32x4*>(head + W_W + 16 * e);
-            if (REV) in.x[j] = *reinterpret_cast<const u32x4*>(head + W_QT + 16 * e);
-            in.K[j] = rk.load(e >> 4, e & 15);
+            in.W[j] = load16(rh, 16 * tid, W_W + 4096 * j);
+            if (REV) in.x[j] = load16(rh, 16 * tid, W_QT + 4096 * j);
+            in.K[j] = rk.load(tid >> 4, tid & 15, 16 * j);
         }
         const Rows<uint16_t> ro(a.dout, nullptr, r0, REV ? rows : 0, a.Hv, vh);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int e = tid + 256 * j, r = e >> 3, q = e & 7;
-            in.c[j] = REV ? ro.load(r, 8 * half + q).v
-                          : *reinterpret_cast<const u32x4*>(head + W_U + r * 256 + 128 * half + 16 * q);
+            const int r = tid >> 3, q = tid & 7;
+            in.c[j] = REV ? ro.load(r, 8 * half + q, 32 * j).v
+                          : load16(rh, r * 256 + 128 * half + 16 * q, W_U + 8192 * j);
         }
         in.gl = reinterpret_cast<const float*>(head + W_G)[C - 1];
     };
     auto put = [&](const Regs& in, byte* S) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = tid + 256 * j, o = granule<256>(e >> 4, e & 15);
+            const int o = staged<256>(tid, j);
             *reinterpret_cast<u32x4*>(S + (REV ? S_R : S_L) + o) = in.W[j];
             *reinterpret_cast<u32x4*>(S + (REV ? S_L : S_R) + o) = in.K[j].bits();
             if (REV) *reinterpret_cast<u32x4*>(S + S_X + o) = in.x[j];
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int e = tid + 256 * j;
-            *reinterpret_cast<u32x4*>(S + S_C + granule<128>(e >> 3, e & 7)) = in.c[j];
+            *reinterpret_cast<u32x4*>(S + S_C + staged<128>(tid, j)) = in.c[j];
         }
         if (tid == 0) *reinterpret_cast<float*>(S + S_G) = in.gl;
     };
@@ -730,7 +732,10 @@ gdn_bwd_spine_kernel(Args a)
 }
 
 // ---- grads -------------------------------------------------------------------------
-constexpr int kGradThreads = 512;
+// Four waves, one to a SIMD, with the registers that this leaves each: the next
+// v-head's matrices wait in them while the present one is worked on, and a wave's
+// tiles are large, which is what the LDS reads go by.
+constexpr int kGradThreads = 256;
 constexpr int G_K = 0;
 constexpr int G_Q = G_K + kTile;
 constexpr int G_DO = G_Q + kTile;
@@ -741,32 +746,33 @@ constexpr int G_X = G_U + kTile;           // T^T and P^T, then dx^T [dv][64]
 constexpr int G_S = G_X + kTile;           // small arrays
 struct Small {
     float G[C], beta[C], ga[C], E[C];      // G in units of log2
-    float rowG[8][C], rowB[8][C];          // by wave
-    float rowX[8][C], colX[8][C], colZ[4][C];
-    float rowQ[4][C];
-    float sumY[8], hd[8];
+    float rowG[4][C], rowB[4][C];          // by wave
+    float rowX[2][C], colX[4][C], colZ[4][C];
+    float rowQ[2][C];
+    float sumY[4], hd[4];
 };
 constexpr int kGradLds = G_S + (int)sizeof(Small);
 static_assert(kGradLds <= 160 * 1024, "the grads kernel's LDS");
 
 template <typename TA>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, 1)
 gdn_bwd_grads_kernel(Args a)
 {
     ChunkAt at;
     const int x = blockIdx.x, kh = blockIdx.y, rep = a.Hv / a.Hk;
     if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, n = lane & 15;
+    int tid = threadIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     byte *sK = lds + G_K, *sQ = lds + G_Q, *sO = lds + G_DO, *sH = lds + G_H, *sDH = lds + G_DH, *sU = lds + G_U,
          *sX = lds + G_X, *sTT = sX, *sPT = sX + kSquare, *sV = sU, *sN = sDH, *sM = sDH + kSquare;
     Small& sm = *reinterpret_cast<Small*>(lds + G_S);
 
-    // a v-head's matrices on their way to LDS
+    // a v-head's matrices on their way to LDS; B's and P's tiles of the rows that
+    // this wave forms of Zu (row tile w) and do u^T (row tile 3 - w)
     struct Regs {
-        u32x4 h[4], dh[4], o[2], tt, pt;
-        Raw<TA> v[2];
-        s16x4 bp[4];
+        u32x4 h[8], dh[8], o[4], tt[2], pt[2];
+        Raw<TA> v[4];
+        s16x4 bb[4], pp[4];
         float G, beta;
     } in;
     auto fetch = [&](int vh) {
@@ -775,60 +781,65 @@ gdn_bwd_grads_kernel(Args a)
         const byte* dhT = a.dh + ((size_t)x * a.Hv + vh) * kState;
         const Rows<TA> rv(a.v, a.v_exps, at.row0, at.rows, a.Hv, vh);
         const Rows<uint16_t> ro(a.dout, nullptr, at.row0, at.rows, a.Hv, vh);
+        const rsrc_t rw = make_rsrc(head, W_BYTES), rh = make_rsrc(hT, kState), rd = make_rsrc(dhT, kState);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            in.h[i] = load16(rh, 16 * tid, 4096 * i);
+            in.dh[i] = load16(rd, 16 * tid, 4096 * i);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            in.h[i] = *reinterpret_cast<const u32x4*>(hT + 16 * (tid + kGradThreads * i));
-            in.dh[i] = *reinterpret_cast<const u32x4*>(dhT + 16 * (tid + kGradThreads * i));
+            in.v[i] = rv.load(tid >> 4, tid & 15, 16 * i);
+            in.o[i] = ro.load(tid >> 4, tid & 15, 16 * i).v;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int e = tid + kGradThreads * i;
-            in.v[i] = rv.load(e >> 4, e & 15);
-            in.o[i] = ro.load(e >> 4, e & 15).v;
+            in.tt[i] = load16(rw, 16 * tid, W_TT + 4096 * i);
+            in.pt[i] = load16(rw, 16 * tid, W_PT + 4096 * i);
         }
-        in.tt = *reinterpret_cast<const u32x4*>(head + W_TT + 16 * tid);
-        in.pt = *reinterpret_cast<const u32x4*>(head + W_PT + 16 * tid);
-        // B's or P's tiles of this wave's block row
-        const int i = w & 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            in.bp[j] = *reinterpret_cast<const s16x4*>(head + (w >= 4 ? W_P : W_B) + 512 * (i * (i + 1) / 2 + min(i, j)) + 8 * lane);
-        in.G = reinterpret_cast<const float*>(head + W_G)[lane];
-        in.beta = reinterpret_cast<const float*>(head + W_G)[C + lane];
+        for (int j = 0; j < 4; ++j) {
+            in.bb[j] = __builtin_bit_cast(s16x4, __builtin_amdgcn_raw_buffer_load_b64(rw, 8 * (tid & 63), W_B + 512 * (w * (w + 1) / 2 + min(w, j)), 0));
+            in.pp[j] = __builtin_bit_cast(s16x4, __builtin_amdgcn_raw_buffer_load_b64(rw, 8 * (tid & 63), W_P + 512 * ((3 - w) * (4 - w) / 2 + min(3 - w, j)), 0));
+        }
+        in.G = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 4 * (tid & 63), W_G, 0));
+        in.beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 4 * (tid & 63), W_G + 4 * C, 0));
     };
     {
         const Rows<TA> rk(a.k, a.k_exps, at.row0, at.rows, a.Hk, kh), rq(a.q, a.q_exps, at.row0, at.rows, a.Hk, kh);
-        Raw<TA> kr[2], qr[2];
+        Raw<TA> kr[4], qr[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = tid + kGradThreads * i;
-            kr[i] = rk.load(e >> 4, e & 15);
-            qr[i] = rq.load(e >> 4, e & 15);
+        for (int i = 0; i < 4; ++i) {
+            kr[i] = rk.load(tid >> 4, tid & 15, 16 * i);
+            qr[i] = rq.load(tid >> 4, tid & 15, 16 * i);
         }
         fetch(kh * rep);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+        for (int i = 0; i < 4; ++i) {
+            const int o = staged<256>(tid, i);
             *reinterpret_cast<u32x4*>(sK + o) = kr[i].bits();
             *reinterpret_cast<u32x4*>(sQ + o) = qr[i].bits();
         }
     }
     Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
-    // dq and dk, transposed: dk columns 32 wc .. + 31 down, rows 32 wr + 16 i + n
-    const int wc = w & 3, wr = w >> 2;
-    f32x4 dq[2][2], dk[2][2];              // [dk tile][row tile]
+    // dq and dk, transposed: dk columns 64 wc .. + 63 down (four tiles under sig),
+    // rows 32 wr + 16 j + n
+    const int wc = w & 1, wr = w >> 1;
+    f32x4 dq[4][2], dk[4][2];              // [dk tile][row tile]
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) dq[i][j] = dk[i][j] = zero4();
 
     for (int vh = kh * rep; vh < (kh + 1) * rep; ++vh) {
         L.fresh();
+        asm volatile("" : "+v"(tid));      // likewise for all that is formed from it
+        const int lane = tid & 63, g = lane >> 4, n = lane & 15;
         lds_barrier();                     // the v-head before has read the LDS
         float hd = 0.f;                    // <h, dh'>
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+        for (int i = 0; i < 8; ++i) {
+            const int o = staged<256>(tid, i);
             *reinterpret_cast<u32x4*>(sH + o) = in.h[i];
             *reinterpret_cast<u32x4*>(sDH + o) = in.dh[i];
 #pragma unroll
@@ -838,19 +849,23 @@ gdn_bwd_grads_kernel(Args a)
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = tid + kGradThreads * i, o = granule<256>(e >> 4, e & 15);
+        for (int i = 0; i < 4; ++i) {
+            const int o = staged<256>(tid, i);
             *reinterpret_cast<u32x4*>(sO + o) = in.o[i];
             *reinterpret_cast<u32x4*>(sV + o) = in.v[i].bits();
         }
-        {
-            const int o = granule<128>(tid >> 3, tid & 7);
-            *reinterpret_cast<u32x4*>(sTT + o) = in.tt;
-            *reinterpret_cast<u32x4*>(sPT + o) = in.pt;
-        }
-        s16x4 bpv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bpv[j] = in.bp[j];
+        for (int i = 0; i < 2; ++i) {
+            const int o = staged<128>(tid, i);
+            *reinterpret_cast<u32x4*>(sTT + o) = in.tt[i];
+            *reinterpret_cast<u32x4*>(sPT + o) = in.pt[i];
+        }
+        s16x4 bb[4], pp[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bb[j] = in.bb[j];
+            pp[j] = in.pp[j];
+        }
         if (w == 0) {
             const float GL = __shfl(in.G, 63);
             sm.G[lane] = in.G;
@@ -863,64 +878,119 @@ gdn_bwd_grads_kernel(Args a)
         if (lane == 0) sm.hd[w] = hd;
         lds_barrier();
 
-        // columns 16 w .. + 15 of dv: x, u, ddelta, dx, rows under sig
-        f32x4 kh4[4], u[4], dd[4], dx[4];
+        // columns 32 w .. + 31 of dv (two tiles): x, u, ddelta, dx, rows under sig
+        f32x4 u[2][4], dx[2][4];
         {
-            f32x4 kd[4];
+            f32x4 kh4[2][4], kd[2][4];
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) kh4[rt] = kd[rt] = zero4();
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) kh4[c][rt] = kd[c][rt] = zero4();
+            s16x8 hb[2][2], db[2][2], kf[2][4];    // by turns of the k-steps
+            auto read = [&](int ks) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    hb[ks & 1][c] = row8<256>(L, G_H, 2 * w + c, ks);
+                    db[ks & 1][c] = row8<256>(L, G_DH, 2 * w + c, ks);
+                }
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) kf[ks & 1][rt] = row8_sig<256>(L, G_K, rt, ks);
+            };
+            s16x8 tf[4][2], pf[4][2], ob[2][2];
+            s16x4 vf[2][4];
+            read(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 hb = row8<256>(L, G_H, w, ks), db = row8<256>(L, G_DH, w, ks);
+                if (ks < 3) {
+                    read(ks + 1);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int rt = 0; rt < 4; ++rt) vf[c][rt] = col4<256>(L, G_U, rt >> 1, rt & 1, 2 * w + c);
+#pragma unroll
+                    for (int rt = 0; rt < 4; ++rt) {
+                        tf[rt][0] = down_sig<128>(L, G_X, 0, rt);            // T lower triangular
+                        if (rt >= 2) tf[rt][1] = down_sig<128>(L, G_X, 1, rt);
+                    }
+                }
+                sched_fence();
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int rt = 0; rt < 4; ++rt) {
+                        kh4[c][rt] = mfma(kf[ks & 1][rt], hb[ks & 1][c], kh4[c][rt]);
+                        kd[c][rt] = mfma(kf[ks & 1][rt], db[ks & 1][c], kd[c][rt]);
+                    }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) ob[c][j] = down<256>(L, G_DO, j, 2 * w + c);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {                                 // P^T upper triangular
+                pf[rt][1] = row8_sig<128>(L, G_X + kSquare, rt, 1);
+                if (rt < 2) pf[rt][0] = row8_sig<128>(L, G_X + kSquare, rt, 0);
+            }
+            sched_fence();
+            f32x4 dd[2][4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f32x4 xv[4];
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) {
-                    const s16x8 kf = row8_sig<256>(L, G_K, rt, ks);
-                    kh4[rt] = mfma(kf, hb, kh4[rt]);
-                    kd[rt] = mfma(kf, db, kd[rt]);
+                    kh4[c][rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
+                    xv[rt] = widen(vf[c][rt]) - kh4[c][rt];
+                }
+                const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    u[c][rt] = mfma(tf[rt][0], xb[0], zero4());
+                    if (rt >= 2) u[c][rt] = mfma(tf[rt][1], xb[1], u[c][rt]);
+                    dd[c][rt] = mfma(pf[rt][1], ob[c][1], zero4());
+                    if (rt < 2) dd[c][rt] = mfma(pf[rt][0], ob[c][0], dd[c][rt]);
                 }
             }
-            f32x4 xv[4];
+            // T^T's rows, in the place of P^T's
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                kh4[rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
-                xv[rt] = widen(col4<256>(L, G_U, rt >> 1, rt & 1, w)) - kh4[rt];
+                pf[rt][1] = row8_sig<128>(L, G_X, rt, 1);
+                if (rt < 2) pf[rt][0] = row8_sig<128>(L, G_X, rt, 0);
             }
-            const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
-            const s16x8 ob[2] = {down<256>(L, G_DO, 0, w), down<256>(L, G_DO, 1, w)};
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                // u = T x (T lower triangular), P^T do (P^T upper triangular)
-                u[rt] = mfma(down_sig<128>(L, G_X, 0, rt), xb[0], zero4());
-                if (rt >= 2) u[rt] = mfma(down_sig<128>(L, G_X, 1, rt), xb[1], u[rt]);
-                dd[rt] = mfma(row8_sig<128>(L, G_X + kSquare, rt, 1), ob[1], zero4());
-                if (rt < 2) dd[rt] = mfma(row8_sig<128>(L, G_X + kSquare, rt, 0), ob[0], dd[rt]);
-            }
-            f32x4 yv[4];
+            sched_fence();
             float sumY = 0.f;
-            f32x4 rY[4];
+            f32x4 rG[4], rB[4];
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const int r = sig0(rt) + 8 * g;
-                const f32x4 E = *reinterpret_cast<const f32x4*>(sm.E + r), bt = *reinterpret_cast<const f32x4*>(sm.beta + r);
-                const f32x4 ek = E * kd[rt];
-                dd[rt] += ek;
-                rY[rt] = bt * u[rt] * ek;
-                yv[rt] = bt * dd[rt];
-            }
-            const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
+            for (int rt = 0; rt < 4; ++rt) rG[rt] = rB[rt] = zero4();
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                dx[rt] = mfma(row8_sig<128>(L, G_X, rt, 1), yb[1], zero4());
-                if (rt < 2) dx[rt] = mfma(row8_sig<128>(L, G_X, rt, 0), yb[0], dx[rt]);
+            for (int c = 0; c < 2; ++c) {
+                f32x4 yv[4];
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    const int r = sig0(rt) + 8 * g;
+                    const f32x4 E = *reinterpret_cast<const f32x4*>(sm.E + r), bt = *reinterpret_cast<const f32x4*>(sm.beta + r);
+                    const f32x4 ek = E * kd[c][rt];
+                    dd[c][rt] += ek;
+                    yv[rt] = bt * dd[c][rt];
+                    rB[rt] += dd[c][rt] * u[c][rt];
+                    const f32x4 Y = bt * u[c][rt] * ek;
+                    rG[rt] -= Y;
+                    sumY += (Y[0] + Y[1]) + (Y[2] + Y[3]);
+                }
+                const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    dx[c][rt] = mfma(pf[rt][1], yb[1], zero4());
+                    if (rt < 2) dx[c][rt] = mfma(pf[rt][0], yb[0], dx[c][rt]);
+                }
             }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 f32x4 rg, rb;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    sumY += rY[rt][s];
-                    rg[s] = sum16(-dx[rt][s] * kh4[rt][s] - rY[rt][s]);
-                    rb[s] = sum16(dd[rt][s] * u[rt][s]);
+                    rg[s] = sum16(rG[rt][s] - dx[0][rt][s] * kh4[0][rt][s] - dx[1][rt][s] * kh4[1][rt][s]);
+                    rb[s] = sum16(rB[rt][s]);
                 }
                 if (n == 0) {
                     *reinterpret_cast<f32x4*>(&sm.rowG[w][sig0(rt) + 8 * g]) = rg;
@@ -931,137 +1001,175 @@ gdn_bwd_grads_kernel(Args a)
             for (int o = 32; o; o >>= 1) sumY += __shfl_xor(sumY, o);
             if (lane == 0) sm.sumY[w] = sumY;
         }
-        lds_barrier();                   // V, T^T and P^T have been read
+        lds_barrier();                     // V, T^T and P^T have been read
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int o = granule<128>(16 * w + n, 4 * j + g);
-            *reinterpret_cast<u32x4*>(sU + o) = pack8(u[2 * j], u[2 * j + 1]);
-            *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[2 * j], dx[2 * j + 1]);
-        }
-        lds_barrier();
-
-        fetch(min(vh + 1, (kh + 1) * rep - 1));   // the next v-head's, while this one is worked on
-        // dv = dx: row tile w % 4, dv columns 64 (w / 4) .. + 63, eight at a time
-        // from transposing reads of dx^T
-        {
-            const int r = 16 * (w & 3) + n;
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 v8 = down<128>(L, G_X, 2 * (w >> 2) + j, w & 3);
-                if (r < at.rows)
-                    *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 64 * (w >> 2) + 32 * j + 8 * g) = v8;
+                const int o = granule<128>(32 * w + 16 * c + n, 4 * j + g);
+                *reinterpret_cast<u32x4*>(sU + o) = pack8(u[c][2 * j], u[c][2 * j + 1]);
+                *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[c][2 * j], dx[c][2 * j + 1]);
             }
-        }
-        // u dh'^T, and then dh' is not needed any more
+        lds_barrier();
+
+        sched_fence();
+        fetch(min(vh + 1, (kh + 1) * rep - 1));   // the next v-head's, while this one is worked on
+        sched_fence();
+
+        // u dh'^T, then do h^T and dx h^T; after them h and dh' are not needed any more
         const int rn[2] = {32 * wr + n, 32 * wr + 16 + n};
         const float ga_n[2] = {sm.ga[rn[0]], sm.ga[rn[1]]};
         {
             const float eb[2] = {sm.E[rn[0]] * sm.beta[rn[0]], sm.E[rn[1]] * sm.beta[rn[1]]};
-            f32x4 t[2][2];
+            f32x4 z[4][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) t[i][j] = zero4();
+                for (int j = 0; j < 2; ++j) z[i][j] = zero4();
+            s16x8 df[2][4], uf[2][2];      // [turn][tile]
+            auto read = [&](int ks) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) df[ks & 1][i] = down_sig<256>(L, G_DH, ks, 4 * wc + i);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) uf[ks & 1][j] = down<128>(L, G_U, ks, 2 * wr + j);
+            };
+            read(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 b0 = down<128>(L, G_U, ks, 2 * wr), b1 = down<128>(L, G_U, ks, 2 * wr + 1);
+                if (ks < 3) read(ks + 1);
+                sched_fence();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const s16x8 af = down_sig<256>(L, G_DH, ks, 2 * wc + i);
-                    t[i][0] = mfma(af, b0, t[i][0]);
-                    t[i][1] = mfma(af, b1, t[i][1]);
-                }
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) z[i][j] = mfma(df[ks & 1][i], uf[ks & 1][j], z[i][j]);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) dk[i][j] += t[i][j] * eb[j];
+                for (int j = 0; j < 2; ++j) dk[i][j] += z[i][j] * eb[j];
         }
-        // do h^T and dx h^T
         {
-            f32x4 t[2][2], y[2][2];
+            f32x4 t[4][2], y[4][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) t[i][j] = y[i][j] = zero4();
+            s16x8 hf[2][4], of[2][2], xf[2][2];
+            auto read = [&](int ks) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hf[ks & 1][i] = down_sig<256>(L, G_H, ks, 4 * wc + i);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    of[ks & 1][j] = row8<256>(L, G_DO, 2 * wr + j, ks);
+                    xf[ks & 1][j] = down<128>(L, G_X, ks, 2 * wr + j);
+                }
+            };
+            read(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const s16x8 o0 = row8<256>(L, G_DO, 2 * wr, ks), o1 = row8<256>(L, G_DO, 2 * wr + 1, ks);
-                const s16x8 x0 = down<128>(L, G_X, ks, 2 * wr), x1 = down<128>(L, G_X, ks, 2 * wr + 1);
+                if (ks < 3) read(ks + 1);
+                sched_fence();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const s16x8 af = down_sig<256>(L, G_H, ks, 2 * wc + i);
-                    t[i][0] = mfma(af, o0, t[i][0]);
-                    t[i][1] = mfma(af, o1, t[i][1]);
-                    y[i][0] = mfma(af, x0, y[i][0]);
-                    y[i][1] = mfma(af, x1, y[i][1]);
-                }
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        t[i][j] = mfma(hf[ks & 1][i], of[ks & 1][j], t[i][j]);
+                        y[i][j] = mfma(hf[ks & 1][i], xf[ks & 1][j], y[i][j]);
+                    }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, wc);
-                const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
                 float s = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const f32x4 d = t[i][j] * ga_n[j];
-                    dq[i][j] += d;
-                    dk[i][j] -= y[i][j] * ga_n[j];
+                for (int p = 0; p < 2; ++p) {
+                    const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, 2 * wc + p);
+                    const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(d[e], i ? q1[e] : q0[e], s);
+                    for (int e = 0; e < 4; ++e) {
+                        s = fmaf(t[2 * p][j][e], q0[e], s);
+                        s = fmaf(t[2 * p + 1][j][e], q1[e], s);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dq[i][j] += t[i][j] * ga_n[j];
+                    dk[i][j] -= y[i][j] * ga_n[j];
                 }
                 s += __shfl_xor(s, 16);
                 s += __shfl_xor(s, 32);
-                if (g == 0) sm.rowQ[wc][rn[j]] = s;
+                if (g == 0) sm.rowQ[wc][rn[j]] = s * ga_n[j];
             }
         }
-        lds_barrier();                   // dh' has been read
+        lds_barrier();                     // h and dh' have been read
 
-        // rows 16 i .. + 15 of Zu (waves 0-3) or do u^T (waves 4-7) on and below
-        // the diagonal: N, dP o Gam, and X's row and column sums
+        // dv = dx: row tile w, eight columns at a time from transposing reads of dx^T
         {
-            const int i = w & 3;
-            const bool isP = w >= 4;
-            s16x8 af[4];
+            const int r = 16 * w + n;
+            s16x8 v8[4];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) af[ks] = isP ? row8<256>(L, G_DO, i, ks) : down<128>(L, G_X, ks, i);
-            const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * i + 4 * g);
-            f32x4 rx = zero4();
-            byte* dst = isP ? sM : sN;
+            for (int j = 0; j < 4; ++j) v8[j] = down<128>(L, G_X, j, w);
+            if (r < at.rows)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f32x4 t = zero4();
-                const int c = 16 * j + n;
-                float cx = 0.f, cz = 0.f;
-                if (j <= i) {
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 32 * j + 8 * g) = v8[j];
+        }
+        // rows 16 w .. + 15 of Zu and 16 (3 - w) .. + 15 of do u^T on and below the
+        // diagonal (five tiles a wave): N, dP o Gam, and X's row and column sums
+        {
+            float cX[4] = {0.f, 0.f, 0.f, 0.f}, cZ[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], down<128>(L, G_U, ks, j), t);
-                    const f32x4 bp = widen(bpv[j]);
-                    const float bt = sm.beta[c], Gc = sm.G[c];
+            for (int half = 0; half < 2; ++half) {
+                const int i = half ? 3 - w : w;
+                s16x8 af[4], uf[2][4];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int r = 16 * i + 4 * g + s;
-                        const bool below = c < r;
-                        const float val = isP ? t[s] * bt : -t[s] * bt;
-                        const float X = below ? val * bp[s] : 0.f;
-                        rx[s] += X;
-                        cx += X;
-                        if (!isP) cz = fmaf(bp[s], below ? t[s] : 0.f, cz);
-                        t[s] = (isP ? c <= r : below) ? val * exp2f(Gr[s] - Gc) : 0.f;
+                for (int ks = 0; ks < 4; ++ks) af[ks] = half ? row8<256>(L, G_DO, i, ks) : down<128>(L, G_X, ks, i);
+                auto read = [&](int j) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) uf[j & 1][ks] = down<128>(L, G_U, ks, j);
+                };
+                read(0);
+                const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * i + 4 * g);
+                f32x4 rx = zero4();
+                byte* dst = half ? sM : sN;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f32x4 t = zero4();
+                    const int c = 16 * j + n;
+                    if (j <= i) {
+                        if (j < 3) read(j + 1);
+                        sched_fence();
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], uf[j & 1][ks], t);
+                        const f32x4 bp = widen(half ? pp[j] : bb[j]);
+                        const float bt = sm.beta[c], Gc = sm.G[c];
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            const int r = 16 * i + 4 * g + s;
+                            const bool below = c < r;
+                            const float val = half ? t[s] * bt : -t[s] * bt;
+                            const float X = below ? val * bp[s] : 0.f;
+                            rx[s] += X;
+                            cX[j] += X;
+                            if (!half) cZ[j] = fmaf(bp[s], below ? t[s] : 0.f, cZ[j]);
+                            t[s] = (half ? c <= r : below) ? val * exp2f(Gr[s] - Gc) : 0.f;
+                        }
                     }
+                    *reinterpret_cast<u32x2*>(dst + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
                 }
-                *reinterpret_cast<u32x2*>(dst + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
-                cx += __shfl_xor(cx, 16); cx += __shfl_xor(cx, 32);
-                if (g == 0) sm.colX[w][c] = cx;
-                if (!isP) {
-                    cz += __shfl_xor(cz, 16); cz += __shfl_xor(cz, 32);
-                    if (g == 0) sm.colZ[w][c] = cz;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float v = sum16(rx[s]);
+                    if (n == 0) sm.rowX[half][16 * i + 4 * g + s] = v;
                 }
             }
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float v = sum16(rx[s]);
-                if (n == 0) sm.rowX[w][16 * i + 4 * g + s] = v;
+            for (int j = 0; j < 4; ++j) {
+                cX[j] += __shfl_xor(cX[j], 16); cX[j] += __shfl_xor(cX[j], 32);
+                cZ[j] += __shfl_xor(cZ[j], 16); cZ[j] += __shfl_xor(cZ[j], 32);
+                if (g == 0) {
+                    sm.colX[w][16 * j + n] = cX[j];
+                    sm.colZ[w][16 * j + n] = cZ[j];
+                }
             }
         }
         lds_barrier();
@@ -1069,44 +1177,50 @@ gdn_bwd_grads_kernel(Args a)
         // (dP o Gam) K to dq; (dP o Gam)^T Q + (N + N^T) K to dk
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            s16x8 kf[2], qf[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                kf[i] = down_sig<256>(L, G_K, ks, 2 * wc + i);
-                qf[i] = down_sig<256>(L, G_Q, ks, 2 * wc + i);
-            }
+            s16x8 kf[4], qf[4], m0[2], m1[2], n0[2], n1[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const s16x8 m0 = down<128>(L, G_DH + kSquare, ks, 2 * wr + j), m1 = row8<128>(L, G_DH + kSquare, 2 * wr + j, ks);
-                const s16x8 n0 = down<128>(L, G_DH, ks, 2 * wr + j), n1 = row8<128>(L, G_DH, 2 * wr + j, ks);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    dq[i][j] = mfma(kf[i], m0, dq[i][j]);
-                    dk[i][j] = mfma(qf[i], m1, dk[i][j]);
-                    dk[i][j] = mfma(kf[i], n0, dk[i][j]);
-                    dk[i][j] = mfma(kf[i], n1, dk[i][j]);
-                }
+                m0[j] = down<128>(L, G_DH + kSquare, ks, 2 * wr + j);
+                n0[j] = down<128>(L, G_DH, ks, 2 * wr + j);
+                n1[j] = row8<128>(L, G_DH, 2 * wr + j, ks);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kf[i] = down_sig<256>(L, G_K, ks, 4 * wc + i);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m1[j] = row8<128>(L, G_DH + kSquare, 2 * wr + j, ks);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[i] = down_sig<256>(L, G_Q, ks, 4 * wc + i);
+            sched_fence();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    dq[i][j] = mfma(kf[i], m0[j], dq[i][j]);
+                    dk[i][j] = mfma(kf[i], n0[j], dk[i][j]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) dk[i][j] = mfma(kf[i], n1[j], dk[i][j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) dk[i][j] = mfma(qf[i], m1[j], dk[i][j]);
         }
         // the gates' gradients
         if (w == 0) {
-            float r = 0.f, bt = 0.f, cx = 0.f, rx = 0.f, cz = 0.f, Y = 0.f, hds = 0.f;
+            float r = 0.f, bt = 0.f, cx = 0.f, cz = 0.f, Y = 0.f, hds = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 r += sm.rowG[i][lane];
                 bt += sm.rowB[i][lane];
                 Y += sm.sumY[i];
                 hds += sm.hd[i];
                 cx += sm.colX[i][lane];
-            }
-            // row tile lane / 16 belongs to waves lane / 16 and lane / 16 + 4
-            rx = sm.rowX[lane >> 4][lane] + sm.rowX[(lane >> 4) + 4][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r += sm.rowQ[i][lane];
                 cz += sm.colZ[i][lane];
             }
-            float d = r + (rx - cx);
+            r += sm.rowQ[0][lane] + sm.rowQ[1][lane];
+            float d = r + ((sm.rowX[0][lane] + sm.rowX[1][lane]) - cx);
             if (lane == C - 1) d += Y + sm.ga[C - 1] * hds;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -1120,14 +1234,17 @@ gdn_bwd_grads_kernel(Args a)
             }
         }
     }
+    const int g = (tid & 63) >> 4, n = tid & 15;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int r = 32 * wr + 16 * j + n;
-        if (r < at.rows) {
-            const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 32 * wc + 8 * g;
-            *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[0][j], dq[1][j]);
-            *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[0][j], dk[1][j]);
-        }
+        if (r < at.rows)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 64 * wc + 32 * p + 8 * g;
+                *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[2 * p][j], dq[2 * p + 1][j]);
+                *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[2 * p][j], dk[2 * p + 1][j]);
+            }
     }
 }
 
