@@ -364,8 +364,8 @@ gdn_bwd_prep_kernel(Args a)
         const float bt = live ? a.beta[r] : 0.f;
         sG[lane] = G;
         sBt[lane] = bt;
-        sGa[lane] = exp2f(G);
-        sEb[lane] = exp2f(GL - G) * bt;
+        sGa[lane] = __builtin_amdgcn_exp2f(G);
+        sEb[lane] = __builtin_amdgcn_exp2f(GL - G) * bt;
         float* gG = reinterpret_cast<float*>(out + W_G);
         gG[lane] = G;
         gG[C + lane] = bt;
@@ -400,7 +400,7 @@ gdn_bwd_prep_kernel(Args a)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const int r = 16 * i + 4 * g + s;
-                        t[s] = (half ? c <= r : c < r) ? t[s] * exp2f(Gr[s] - Gc) : 0.f;
+                        t[s] = (half ? c <= r : c < r) ? t[s] * __builtin_amdgcn_exp2f(Gr[s] - Gc) : 0.f;
                     }
                     const int tile = i * (i + 1) / 2 + j;
                     *reinterpret_cast<u32x2*>(out + (half ? W_P : W_B) + 512 * tile + 8 * lane) = pack4(t);
@@ -656,7 +656,7 @@ __device__ __forceinline__ void spine_walk(const Args& a)
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) lf[rt][ks] = row8_sig<256>(L, S + S_L, rt, ks);
-        const float gl = exp2f(*reinterpret_cast<const float*>(lds + S + S_G));
+        const float gl = __builtin_amdgcn_exp2f(*reinterpret_cast<const float*>(lds + S + S_G));
         sched_fence();
 
         const int c = REV ? nc - 1 - i : i;
@@ -732,10 +732,9 @@ gdn_bwd_spine_kernel(Args a)
 }
 
 // ---- grads -------------------------------------------------------------------------
-// Four waves, one to a SIMD, with the registers that this leaves each: the next
-// v-head's matrices wait in them while the present one is worked on, and a wave's
-// tiles are large, which is what the LDS reads go by.
-constexpr int kGradThreads = 256;
+// Eight waves, two to a SIMD, so that one's products run under the other's vector
+// work and LDS reads.
+constexpr int kGradThreads = 512;
 constexpr int G_K = 0;
 constexpr int G_Q = G_K + kTile;
 constexpr int G_DO = G_Q + kTile;
@@ -746,16 +745,16 @@ constexpr int G_X = G_U + kTile;           // T^T and P^T, then dx^T [dv][64]
 constexpr int G_S = G_X + kTile;           // small arrays
 struct Small {
     float G[C], beta[C], ga[C], E[C];      // G in units of log2
-    float rowG[4][C], rowB[4][C];          // by wave
-    float rowX[2][C], colX[4][C], colZ[4][C];
-    float rowQ[2][C];
-    float sumY[4], hd[4];
+    float rowG[8][C], rowB[8][C];          // by wave
+    float rowX[2][C], colX[8][C], colZ[4][C];
+    float rowQ[4][C];
+    float sumY[8], hd[8];
 };
 constexpr int kGradLds = G_S + (int)sizeof(Small);
 static_assert(kGradLds <= 160 * 1024, "the grads kernel's LDS");
 
 template <typename TA>
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(kGradThreads)
 gdn_bwd_grads_kernel(Args a)
 {
     ChunkAt at;
@@ -767,14 +766,15 @@ gdn_bwd_grads_kernel(Args a)
          *sX = lds + G_X, *sTT = sX, *sPT = sX + kSquare, *sV = sU, *sN = sDH, *sM = sDH + kSquare;
     Small& sm = *reinterpret_cast<Small*>(lds + G_S);
 
-    // a v-head's matrices on their way to LDS; B's and P's tiles of the rows that
-    // this wave forms of Zu (row tile w) and do u^T (row tile 3 - w)
+    // a v-head's matrices on their way to LDS; B's or P's tiles of the rows that
+    // this wave forms of Zu (waves 0-3, row tile w) or do u^T (row tile 7 - w)
     struct Regs {
-        u32x4 h[8], dh[8], o[4], tt[2], pt[2];
-        Raw<TA> v[4];
-        s16x4 bb[4], pp[4];
+        u32x4 h[4], dh[4], o[2], tt, pt;
+        Raw<TA> v[2];
+        s16x4 bp[4];
         float G, beta;
     } in;
+    const int ti = w >= 4 ? 7 - w : w;     // row tile of Zu or do u^T: with its SIMD's other wave, five tiles
     auto fetch = [&](int vh) {
         const byte* head = a.heads + ((size_t)x * a.Hv + vh) * W_BYTES;
         const byte* hT = a.h + ((size_t)x * a.Hv + vh) * kState;
@@ -783,51 +783,47 @@ gdn_bwd_grads_kernel(Args a)
         const Rows<uint16_t> ro(a.dout, nullptr, at.row0, at.rows, a.Hv, vh);
         const rsrc_t rw = make_rsrc(head, W_BYTES), rh = make_rsrc(hT, kState), rd = make_rsrc(dhT, kState);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            in.h[i] = load16(rh, 16 * tid, 4096 * i);
-            in.dh[i] = load16(rd, 16 * tid, 4096 * i);
-        }
-#pragma unroll
         for (int i = 0; i < 4; ++i) {
-            in.v[i] = rv.load(tid >> 4, tid & 15, 16 * i);
-            in.o[i] = ro.load(tid >> 4, tid & 15, 16 * i).v;
+            in.h[i] = load16(rh, 16 * tid, 8192 * i);
+            in.dh[i] = load16(rd, 16 * tid, 8192 * i);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            in.tt[i] = load16(rw, 16 * tid, W_TT + 4096 * i);
-            in.pt[i] = load16(rw, 16 * tid, W_PT + 4096 * i);
+            in.v[i] = rv.load(tid >> 4, tid & 15, 32 * i);
+            in.o[i] = ro.load(tid >> 4, tid & 15, 32 * i).v;
         }
+        in.tt = load16(rw, 16 * tid, W_TT);
+        in.pt = load16(rw, 16 * tid, W_PT);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            in.bb[j] = __builtin_bit_cast(s16x4, __builtin_amdgcn_raw_buffer_load_b64(rw, 8 * (tid & 63), W_B + 512 * (w * (w + 1) / 2 + min(w, j)), 0));
-            in.pp[j] = __builtin_bit_cast(s16x4, __builtin_amdgcn_raw_buffer_load_b64(rw, 8 * (tid & 63), W_P + 512 * ((3 - w) * (4 - w) / 2 + min(3 - w, j)), 0));
+            in.bp[j] = __builtin_bit_cast(s16x4, __builtin_amdgcn_raw_buffer_load_b64(
+                rw, 8 * (tid & 63), (w >= 4 ? W_P : W_B) + 512 * (ti * (ti + 1) / 2 + min(ti, j)), 0));
         }
         in.G = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 4 * (tid & 63), W_G, 0));
         in.beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, 4 * (tid & 63), W_G + 4 * C, 0));
     };
     {
         const Rows<TA> rk(a.k, a.k_exps, at.row0, at.rows, a.Hk, kh), rq(a.q, a.q_exps, at.row0, at.rows, a.Hk, kh);
-        Raw<TA> kr[4], qr[4];
+        Raw<TA> kr[2], qr[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            kr[i] = rk.load(tid >> 4, tid & 15, 16 * i);
-            qr[i] = rq.load(tid >> 4, tid & 15, 16 * i);
+        for (int i = 0; i < 2; ++i) {
+            kr[i] = rk.load(tid >> 4, tid & 15, 32 * i);
+            qr[i] = rq.load(tid >> 4, tid & 15, 32 * i);
         }
-        fetch(kh * rep);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int o = staged<256>(tid, i);
+        for (int i = 0; i < 2; ++i) {
+            const int o = granule<256>(tid >> 4, tid & 15) + 8192 * i;
             *reinterpret_cast<u32x4*>(sK + o) = kr[i].bits();
             *reinterpret_cast<u32x4*>(sQ + o) = qr[i].bits();
         }
     }
     Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
-    // dq and dk, transposed: dk columns 64 wc .. + 63 down (four tiles under sig),
+    // dq and dk, transposed: dk columns 32 wc .. + 31 down (two tiles under sig),
     // rows 32 wr + 16 j + n
-    const int wc = w & 1, wr = w >> 1;
-    f32x4 dq[4][2], dk[4][2];              // [dk tile][row tile]
+    const int wc = w & 3, wr = w >> 2;
+    f32x4 dq[2][2], dk[2][2];              // [dk tile][row tile]
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) dq[i][j] = dk[i][j] = zero4();
 
@@ -835,11 +831,12 @@ gdn_bwd_grads_kernel(Args a)
         L.fresh();
         asm volatile("" : "+v"(tid));      // likewise for all that is formed from it
         const int lane = tid & 63, g = lane >> 4, n = lane & 15;
+        fetch(vh);
         lds_barrier();                     // the v-head before has read the LDS
         float hd = 0.f;                    // <h, dh'>
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int o = staged<256>(tid, i);
+        for (int i = 0; i < 4; ++i) {
+            const int o = granule<256>(tid >> 4, tid & 15) + 8192 * i;
             *reinterpret_cast<u32x4*>(sH + o) = in.h[i];
             *reinterpret_cast<u32x4*>(sDH + o) = in.dh[i];
 #pragma unroll
@@ -849,55 +846,48 @@ gdn_bwd_grads_kernel(Args a)
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int o = staged<256>(tid, i);
+        for (int i = 0; i < 2; ++i) {
+            const int o = granule<256>(tid >> 4, tid & 15) + 8192 * i;
             *reinterpret_cast<u32x4*>(sO + o) = in.o[i];
             *reinterpret_cast<u32x4*>(sV + o) = in.v[i].bits();
         }
+        *reinterpret_cast<u32x4*>(sTT + granule<128>(tid >> 3, tid & 7)) = in.tt;
+        *reinterpret_cast<u32x4*>(sPT + granule<128>(tid >> 3, tid & 7)) = in.pt;
+        s16x4 bp4[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int o = staged<128>(tid, i);
-            *reinterpret_cast<u32x4*>(sTT + o) = in.tt[i];
-            *reinterpret_cast<u32x4*>(sPT + o) = in.pt[i];
-        }
-        s16x4 bb[4], pp[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            bb[j] = in.bb[j];
-            pp[j] = in.pp[j];
-        }
+        for (int j = 0; j < 4; ++j) bp4[j] = in.bp[j];
         if (w == 0) {
             const float GL = __shfl(in.G, 63);
             sm.G[lane] = in.G;
             sm.beta[lane] = in.beta;
-            sm.ga[lane] = exp2f(in.G);
-            sm.E[lane] = exp2f(GL - in.G);
+            sm.ga[lane] = __builtin_amdgcn_exp2f(in.G);
+            sm.E[lane] = __builtin_amdgcn_exp2f(GL - in.G);
         }
 #pragma unroll
         for (int o = 32; o; o >>= 1) hd += __shfl_xor(hd, o);
         if (lane == 0) sm.hd[w] = hd;
         lds_barrier();
 
-        // columns 32 w .. + 31 of dv (two tiles): x, u, ddelta, dx, rows under sig
-        f32x4 u[2][4], dx[2][4];
+        // columns 16 w .. + 15 of dv: x, u, ddelta, dx, rows under sig
+        f32x4 u[1][4], dx[1][4];
         {
-            f32x4 kh4[2][4], kd[2][4];
+            f32x4 kh4[1][4], kd[1][4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 1; ++c)
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) kh4[c][rt] = kd[c][rt] = zero4();
-            s16x8 hb[2][2], db[2][2], kf[2][4];    // by turns of the k-steps
+            s16x8 hb[2][1], db[2][1], kf[2][4];    // by turns of the k-steps
             auto read = [&](int ks) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    hb[ks & 1][c] = row8<256>(L, G_H, 2 * w + c, ks);
-                    db[ks & 1][c] = row8<256>(L, G_DH, 2 * w + c, ks);
+                for (int c = 0; c < 1; ++c) {
+                    hb[ks & 1][c] = row8<256>(L, G_H, w + c, ks);
+                    db[ks & 1][c] = row8<256>(L, G_DH, w + c, ks);
                 }
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) kf[ks & 1][rt] = row8_sig<256>(L, G_K, rt, ks);
             };
-            s16x8 tf[4][2], pf[4][2], ob[2][2];
-            s16x4 vf[2][4];
+            s16x8 tf[4][2], pf[4][2], ob[1][2];
+            s16x4 vf[1][4];
             read(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -905,9 +895,9 @@ gdn_bwd_grads_kernel(Args a)
                     read(ks + 1);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 1; ++c)
 #pragma unroll
-                        for (int rt = 0; rt < 4; ++rt) vf[c][rt] = col4<256>(L, G_U, rt >> 1, rt & 1, 2 * w + c);
+                        for (int rt = 0; rt < 4; ++rt) vf[c][rt] = col4<256>(L, G_U, rt >> 1, rt & 1, w + c);
 #pragma unroll
                     for (int rt = 0; rt < 4; ++rt) {
                         tf[rt][0] = down_sig<128>(L, G_X, 0, rt);            // T lower triangular
@@ -916,7 +906,7 @@ gdn_bwd_grads_kernel(Args a)
                 }
                 sched_fence();
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 1; ++c)
 #pragma unroll
                     for (int rt = 0; rt < 4; ++rt) {
                         kh4[c][rt] = mfma(kf[ks & 1][rt], hb[ks & 1][c], kh4[c][rt]);
@@ -924,18 +914,18 @@ gdn_bwd_grads_kernel(Args a)
                     }
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 1; ++c)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) ob[c][j] = down<256>(L, G_DO, j, 2 * w + c);
+                for (int j = 0; j < 2; ++j) ob[c][j] = down<256>(L, G_DO, j, w + c);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {                                 // P^T upper triangular
                 pf[rt][1] = row8_sig<128>(L, G_X + kSquare, rt, 1);
                 if (rt < 2) pf[rt][0] = row8_sig<128>(L, G_X + kSquare, rt, 0);
             }
             sched_fence();
-            f32x4 dd[2][4];
+            f32x4 dd[1][4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 1; ++c) {
                 f32x4 xv[4];
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) {
@@ -963,7 +953,7 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) rG[rt] = rB[rt] = zero4();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 1; ++c) {
                 f32x4 yv[4];
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) {
@@ -989,7 +979,7 @@ gdn_bwd_grads_kernel(Args a)
                 f32x4 rg, rb;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    rg[s] = sum16(rG[rt][s] - dx[0][rt][s] * kh4[0][rt][s] - dx[1][rt][s] * kh4[1][rt][s]);
+                    rg[s] = sum16(rG[rt][s] - dx[0][rt][s] * kh4[0][rt][s]);
                     rb[s] = sum16(rB[rt][s]);
                 }
                 if (n == 0) {
@@ -1003,33 +993,30 @@ gdn_bwd_grads_kernel(Args a)
         }
         lds_barrier();                     // V, T^T and P^T have been read
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 1; ++c)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int o = granule<128>(32 * w + 16 * c + n, 4 * j + g);
+                const int o = granule<128>(16 * w + n, 4 * j + g);
                 *reinterpret_cast<u32x4*>(sU + o) = pack8(u[c][2 * j], u[c][2 * j + 1]);
                 *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[c][2 * j], dx[c][2 * j + 1]);
             }
         lds_barrier();
 
-        sched_fence();
-        fetch(min(vh + 1, (kh + 1) * rep - 1));   // the next v-head's, while this one is worked on
-        sched_fence();
 
         // u dh'^T, then do h^T and dx h^T; after them h and dh' are not needed any more
         const int rn[2] = {32 * wr + n, 32 * wr + 16 + n};
         const float ga_n[2] = {sm.ga[rn[0]], sm.ga[rn[1]]};
         {
             const float eb[2] = {sm.E[rn[0]] * sm.beta[rn[0]], sm.E[rn[1]] * sm.beta[rn[1]]};
-            f32x4 z[4][2];
+            f32x4 z[2][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) z[i][j] = zero4();
-            s16x8 df[2][4], uf[2][2];      // [turn][tile]
+            s16x8 df[2][2], uf[2][2];      // [turn][tile]
             auto read = [&](int ks) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) df[ks & 1][i] = down_sig<256>(L, G_DH, ks, 4 * wc + i);
+                for (int i = 0; i < 2; ++i) df[ks & 1][i] = down_sig<256>(L, G_DH, ks, 2 * wc + i);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) uf[ks & 1][j] = down<128>(L, G_U, ks, 2 * wr + j);
             };
@@ -1039,25 +1026,25 @@ gdn_bwd_grads_kernel(Args a)
                 if (ks < 3) read(ks + 1);
                 sched_fence();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) z[i][j] = mfma(df[ks & 1][i], uf[ks & 1][j], z[i][j]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) dk[i][j] += z[i][j] * eb[j];
         }
         {
-            f32x4 t[4][2], y[4][2];
+            f32x4 t[2][2], y[2][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) t[i][j] = y[i][j] = zero4();
-            s16x8 hf[2][4], of[2][2], xf[2][2];
+            s16x8 hf[2][2], of[2][2], xf[2][2];
             auto read = [&](int ks) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) hf[ks & 1][i] = down_sig<256>(L, G_H, ks, 4 * wc + i);
+                for (int i = 0; i < 2; ++i) hf[ks & 1][i] = down_sig<256>(L, G_H, ks, 2 * wc + i);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     of[ks & 1][j] = row8<256>(L, G_DO, 2 * wr + j, ks);
@@ -1070,7 +1057,7 @@ gdn_bwd_grads_kernel(Args a)
                 if (ks < 3) read(ks + 1);
                 sched_fence();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         t[i][j] = mfma(hf[ks & 1][i], of[ks & 1][j], t[i][j]);
@@ -1081,8 +1068,8 @@ gdn_bwd_grads_kernel(Args a)
             for (int j = 0; j < 2; ++j) {
                 float s = 0.f;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, 2 * wc + p);
+                for (int p = 0; p < 1; ++p) {
+                    const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, wc);
                     const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -1091,7 +1078,7 @@ gdn_bwd_grads_kernel(Args a)
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     dq[i][j] += t[i][j] * ga_n[j];
                     dk[i][j] -= y[i][j] * ga_n[j];
                 }
@@ -1102,74 +1089,67 @@ gdn_bwd_grads_kernel(Args a)
         }
         lds_barrier();                     // h and dh' have been read
 
-        // dv = dx: row tile w, eight columns at a time from transposing reads of dx^T
+        // dv = dx: row tile w % 4, dv columns 64 (w / 4) .. + 63, eight columns at a time from transposing reads of dx^T
         {
-            const int r = 16 * w + n;
-            s16x8 v8[4];
+            const int r = 16 * (w & 3) + n;
+            s16x8 v8[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v8[j] = down<128>(L, G_X, j, w);
+            for (int j = 0; j < 2; ++j) v8[j] = down<128>(L, G_X, 2 * (w >> 2) + j, w & 3);
             if (r < at.rows)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 32 * j + 8 * g) = v8[j];
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<s16x8*>(a.dv + ((at.row0 + r) * a.Hv + vh) * D + 64 * (w >> 2) + 32 * j + 8 * g) = v8[j];
         }
-        // rows 16 w .. + 15 of Zu and 16 (3 - w) .. + 15 of do u^T on and below the
-        // diagonal (five tiles a wave): N, dP o Gam, and X's row and column sums
+        // rows 16 ti .. + 15 of Zu or do u^T on and below the diagonal: N or dP o
+        // Gam, and X's row and column sums
         {
-            float cX[4] = {0.f, 0.f, 0.f, 0.f}, cZ[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool isP = w >= 4;
+            s16x8 af[4], uf[2][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = half ? 3 - w : w;
-                s16x8 af[4], uf[2][4];
+            for (int ks = 0; ks < 4; ++ks) af[ks] = isP ? row8<256>(L, G_DO, ti, ks) : down<128>(L, G_X, ks, ti);
+            auto read = [&](int j) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) af[ks] = half ? row8<256>(L, G_DO, i, ks) : down<128>(L, G_X, ks, i);
-                auto read = [&](int j) {
+                for (int ks = 0; ks < 4; ++ks) uf[j & 1][ks] = down<128>(L, G_U, ks, j);
+            };
+            read(0);
+            const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * ti + 4 * g);
+            f32x4 rx = zero4();
+            byte* dst = isP ? sM : sN;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) uf[j & 1][ks] = down<128>(L, G_U, ks, j);
-                };
-                read(0);
-                const f32x4 Gr = *reinterpret_cast<const f32x4*>(sm.G + 16 * i + 4 * g);
-                f32x4 rx = zero4();
-                byte* dst = half ? sM : sN;
+            for (int j = 0; j < 4; ++j) {
+                f32x4 t = zero4();
+                const int c = 16 * j + n;
+                float cx = 0.f, cz = 0.f;
+                if (j <= ti) {
+                    if (j < 3) read(j + 1);
+                    sched_fence();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f32x4 t = zero4();
-                    const int c = 16 * j + n;
-                    if (j <= i) {
-                        if (j < 3) read(j + 1);
-                        sched_fence();
+                    for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], uf[j & 1][ks], t);
+                    const f32x4 bp = widen(bp4[j]);
+                    const float bt = isP ? sm.beta[c] : -sm.beta[c], Gc = sm.G[c];
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) t = mfma(af[ks], uf[j & 1][ks], t);
-                        const f32x4 bp = widen(half ? pp[j] : bb[j]);
-                        const float bt = sm.beta[c], Gc = sm.G[c];
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            const int r = 16 * i + 4 * g + s;
-                            const bool below = c < r;
-                            const float val = half ? t[s] * bt : -t[s] * bt;
-                            const float X = below ? val * bp[s] : 0.f;
-                            rx[s] += X;
-                            cX[j] += X;
-                            if (!half) cZ[j] = fmaf(bp[s], below ? t[s] : 0.f, cZ[j]);
-                            t[s] = (half ? c <= r : below) ? val * exp2f(Gr[s] - Gc) : 0.f;
-                        }
+                    for (int s = 0; s < 4; ++s) {
+                        const int r = 16 * ti + 4 * g + s;
+                        // B's and, in the mask, P's entries from the diagonal on are zero
+                        const float b = c < r ? bp[s] : 0.f, val = t[s] * bt;
+                        cz = fmaf(b, t[s], cz);
+                        rx[s] = fmaf(val, b, rx[s]);
+                        cx = fmaf(val, b, cx);
+                        t[s] = (isP ? c <= r : c < r) ? val * __builtin_amdgcn_exp2f(Gr[s] - Gc) : 0.f;
                     }
-                    *reinterpret_cast<u32x2*>(dst + granule<128>(c, 2 * i + (g >> 1)) + 8 * (g & 1)) = pack4(t);
                 }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float v = sum16(rx[s]);
-                    if (n == 0) sm.rowX[half][16 * i + 4 * g + s] = v;
+                *reinterpret_cast<u32x2*>(dst + granule<128>(c, 2 * ti + (g >> 1)) + 8 * (g & 1)) = pack4(t);
+                cx += __shfl_xor(cx, 16); cx += __shfl_xor(cx, 32);
+                if (g == 0) sm.colX[w][c] = cx;
+                if (!isP) {
+                    cz += __shfl_xor(cz, 16); cz += __shfl_xor(cz, 32);
+                    if (g == 0) sm.colZ[w][c] = cz;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                cX[j] += __shfl_xor(cX[j], 16); cX[j] += __shfl_xor(cX[j], 32);
-                cZ[j] += __shfl_xor(cZ[j], 16); cZ[j] += __shfl_xor(cZ[j], 32);
-                if (g == 0) {
-                    sm.colX[w][16 * j + n] = cX[j];
-                    sm.colZ[w][16 * j + n] = cZ[j];
-                }
+            for (int s = 0; s < 4; ++s) {
+                const float v = sum16(rx[s]);
+                if (n == 0) sm.rowX[isP][16 * ti + 4 * g + s] = v;
             }
         }
         lds_barrier();
@@ -1177,7 +1157,7 @@ gdn_bwd_grads_kernel(Args a)
         // (dP o Gam) K to dq; (dP o Gam)^T Q + (N + N^T) K to dk
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            s16x8 kf[4], qf[4], m0[2], m1[2], n0[2], n1[2];
+            s16x8 kf[2], qf[2], m0[2], m1[2], n0[2], n1[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 m0[j] = down<128>(L, G_DH + kSquare, ks, 2 * wr + j);
@@ -1185,25 +1165,25 @@ gdn_bwd_grads_kernel(Args a)
                 n1[j] = row8<128>(L, G_DH, 2 * wr + j, ks);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) kf[i] = down_sig<256>(L, G_K, ks, 4 * wc + i);
+            for (int i = 0; i < 2; ++i) kf[i] = down_sig<256>(L, G_K, ks, 2 * wc + i);
 #pragma unroll
             for (int j = 0; j < 2; ++j) m1[j] = row8<128>(L, G_DH + kSquare, 2 * wr + j, ks);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[i] = down_sig<256>(L, G_Q, ks, 4 * wc + i);
+            for (int i = 0; i < 2; ++i) qf[i] = down_sig<256>(L, G_Q, ks, 2 * wc + i);
             sched_fence();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     dq[i][j] = mfma(kf[i], m0[j], dq[i][j]);
                     dk[i][j] = mfma(kf[i], n0[j], dk[i][j]);
                 }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) dk[i][j] = mfma(kf[i], n1[j], dk[i][j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) dk[i][j] = mfma(qf[i], m1[j], dk[i][j]);
         }
@@ -1211,15 +1191,18 @@ gdn_bwd_grads_kernel(Args a)
         if (w == 0) {
             float r = 0.f, bt = 0.f, cx = 0.f, cz = 0.f, Y = 0.f, hds = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 r += sm.rowG[i][lane];
                 bt += sm.rowB[i][lane];
                 Y += sm.sumY[i];
                 hds += sm.hd[i];
                 cx += sm.colX[i][lane];
-                cz += sm.colZ[i][lane];
             }
-            r += sm.rowQ[0][lane] + sm.rowQ[1][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cz += sm.colZ[i][lane];
+                r += sm.rowQ[i][lane];
+            }
             float d = r + ((sm.rowX[0][lane] + sm.rowX[1][lane]) - cx);
             if (lane == C - 1) d += Y + sm.ga[C - 1] * hds;
 #pragma unroll
@@ -1240,8 +1223,8 @@ gdn_bwd_grads_kernel(Args a)
         const int r = 32 * wr + 16 * j + n;
         if (r < at.rows)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 64 * wc + 32 * p + 8 * g;
+            for (int p = 0; p < 1; ++p) {
+                const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 32 * wc + 8 * g;
                 *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[2 * p][j], dq[2 * p + 1][j]);
                 *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[2 * p][j], dk[2 * p + 1][j]);
             }
