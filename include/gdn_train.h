@@ -87,7 +87,8 @@ int gdn_ckpt8_load_plan(const uint8_t* codes, const uint8_t* exps, void* y, int6
  * values the codes stand for.  io_dtype is the type of dy, dx, dz.  dw is
  * required; db is required exactly when b is given, dz exactly when z is.
  * T == 0 writes zeros to dw and db.
- * workspace: gdn_norm_workspace_bytes(T, H, d) bytes (fp32 partial sums).
+ * workspace: gdn_norm_workspace_bytes(T, H, d) bytes (fp32 partial sums),
+ * aligned to 16 bytes.
  *
  * Limits: T >= 0, H >= 1, 1 <= d <= 8192, T * H < 2^31, eps >= 0 and finite.
  * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DIM_LIMIT (d),

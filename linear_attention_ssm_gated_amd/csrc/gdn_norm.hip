@@ -85,6 +85,56 @@ template <int VEC> __device__ __forceinline__ void store_vec(uint16_t* p, const 
         *p = f32_to_bf16_bits(f[0]);
 }
 
+// The same values as they lie in memory, fetched ahead of their use.
+template <int VEC, typename T> struct RawVec {
+    static constexpr int W = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 4) w[0] = __float_as_uint(*reinterpret_cast<const float*>(p));
+            else w[0] = (uint32_t)*p;
+        } else if constexpr (W >= 4) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const u4 v = *reinterpret_cast<const u4*>(reinterpret_cast<const uint32_t*>(p) + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+            }
+        } else {
+            const u2 v = *reinterpret_cast<const u2*>(p);
+            w[0] = v[0];
+            w[1] = v[1];
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void widen(float* f) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(w[i]);
+        } else if constexpr (sizeof(T) == 2) {
+            if constexpr (VEC == 1) f[0] = __uint_as_float(w[0] << 16);
+            else
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) {
+                    f[2 * i] = __uint_as_float(w[i] << 16);
+                    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                }
+        } else {
+            if constexpr (VEC == 1) f[0] = ckpt_unpack1((uint8_t)w[0]);
+            else {
+                ckpt_unpack4(w[0], f);
+                ckpt_unpack4(w[1], f + 4);
+            }
+        }
+    }
+};
+
 // ---- sums over the TPR threads of a row --------------------------------------
 // slot: a different one for each reduction of a row (LDS, TPR > 64 only); two
 // reductions a row keep a slot's readers ahead of its next writers.
@@ -104,7 +154,13 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red,
     return x;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// The hardware's exp2 and reciprocal, within one unit in the last place each: a
+// relative error of a few 2^-24, where the correctly rounded division alone
+// took ten instructions of the thirty-five that a gated value needs in all.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
 
 struct Shape {
     int64_t rows;
@@ -113,12 +169,30 @@ struct Shape {
     int center;
 };
 
-__device__ __forceinline__ int64_t row_at(int64_t row, const Shape& s, int64_t stride)
-{
-    if (s.H == 1) return row * stride;
-    const uint32_t t = (uint32_t)row / (uint32_t)s.H;
-    return (int64_t)t * stride + (int64_t)((uint32_t)row - t * (uint32_t)s.H) * s.d;
-}
+// Where a row group is: token and head, moved on by a fixed number of rows
+// without a division.
+struct Place {
+    int64_t row;
+    int t, h;
+    __device__ __forceinline__ Place(int64_t r, const Shape& s) : row(r), t((int)r), h(0)
+    {
+        if (s.H > 1) {
+            t = (int)((uint32_t)r / (uint32_t)s.H);
+            h = (int)((uint32_t)r - (uint32_t)t * (uint32_t)s.H);
+        }
+    }
+    __device__ __forceinline__ void move(int rows, int dt, int dh, const Shape& s)
+    {
+        row += rows;
+        t += dt;
+        h += dh;
+        if (h >= s.H) {
+            h -= s.H;
+            ++t;
+        }
+    }
+    __device__ __forceinline__ int64_t at(int64_t stride, const Shape& s) const { return (int64_t)t * stride + h * s.d; }
+};
 
 // The row's values minus their mean (center), and 1 / sqrt(var + eps).
 template <int TPR, int NV, int VEC>
@@ -139,7 +213,7 @@ __device__ __forceinline__ float normalise(float* x, const Shape& s, int l, floa
 #pragma unroll
     for (int e = 0; e < NV * VEC; ++e) q = fmaf(x[e], x[e], q);
     q = row_sum<TPR>(q, red, 1) * s.inv_d;
-    return 1.0f / sqrtf(q + s.eps);
+    return __builtin_amdgcn_rsqf(q + s.eps);
 }
 
 // Codes and scale byte of the VEC = 8 values of each lane, a group's 128 lying
@@ -172,7 +246,7 @@ __device__ __forceinline__ void write_codes(const float* x, uint8_t* codes, uint
 }
 
 // ---- forward -----------------------------------------------------------------
-template <typename T, int TPR, int NV, int VEC>
+template <typename T, int TPR, int NV, int VEC, bool GATE>
 __global__ void __launch_bounds__(wg_threads(TPR))
 gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const float* __restrict__ w,
                         const float* __restrict__ b, T* __restrict__ y, uint8_t* __restrict__ x_codes,
@@ -183,33 +257,39 @@ gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const 
     __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
     constexpr int RPW = wg_threads(TPR) / TPR;
     const int l = threadIdx.x % TPR;
+    const int step = (int)gridDim.x * RPW, dt = step / s.H, dh = step - dt * s.H;
+    Place p((int64_t)blockIdx.x * RPW + threadIdx.x / TPR, s);
     int turn = 0;
-    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += (int64_t)gridDim.x * RPW) {
-        const int64_t row = base + threadIdx.x / TPR;
-        const bool live = row < s.rows;   // a dead row group still takes part in the lane exchanges
-        const T* px = x + (live ? row_at(row, s, x_stride) : 0);
-        const T* pz = z ? z + (live ? row_at(row, s, z_stride) : 0) : nullptr;
-        float xv[NV * VEC], zv[NV * VEC];
+    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += step, p.move(step, dt, dh, s)) {
+        const bool live = p.row < s.rows;   // a dead row group still takes part in the lane exchanges
+        float xv[NV * VEC], zv[GATE ? NV * VEC : 1];
+        RawVec<VEC, T> rx[NV], rz[GATE ? NV : 1];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * TPR + l) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) xv[i * VEC + e] = zv[i * VEC + e] = 0.f;
+            rx[i].zero();
+            if constexpr (GATE) rz[i].zero();
             if (live && j < s.d) {
-                load_vec<VEC>(px + j, xv + i * VEC);
-                if (pz) load_vec<VEC>(pz + j, zv + i * VEC);
+                rx[i].load(x + p.at(x_stride, s) + j);
+                if constexpr (GATE) rz[i].load(z + p.at(z_stride, s) + j);
             }
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            rx[i].widen(xv + i * VEC);
+            if constexpr (GATE) rz[i].widen(zv + i * VEC);
+        }
         if constexpr (VEC == 8) {
-            if (live && x_codes) write_codes<TPR, NV>(xv, x_codes, x_exps, row, s, l);
-            if (live && z_codes) write_codes<TPR, NV>(zv, z_codes, z_exps, row, s, l);
+            if (live && x_codes) write_codes<TPR, NV>(xv, x_codes, x_exps, p.row, s, l);
+            if constexpr (GATE)
+                if (live && z_codes) write_codes<TPR, NV>(zv, z_codes, z_exps, p.row, s, l);
         }
         // LDS slots by turns: an RMS norm's one reduction a row would let the
         // next row's writers overtake this row's readers
         const float r = normalise<TPR, NV, VEC>(xv, s, l, red + 2 * kMaxWaves * turn);
         turn = TPR > 64 ? turn ^ 1 : 0;
         if (!live) continue;
-        T* py = y + row_at(row, s, y_stride);
+        T* py = y + p.at(y_stride, s);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * TPR + l) * VEC;
@@ -221,8 +301,11 @@ gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const 
             for (int e = 0; e < VEC; ++e) {
                 float a = xv[i * VEC + e] * r * wv[e];
                 if (b) a += bv[e];
-                const float zz = zv[i * VEC + e];
-                o[e] = pz ? a * (zz * sigmoid(zz)) : a;
+                if constexpr (GATE) {
+                    const float zz = zv[i * VEC + e];
+                    a *= zz * sigmoid(zz);
+                }
+                o[e] = a;
             }
             store_vec<VEC>(py + j, o);
         }
@@ -230,8 +313,9 @@ gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const 
 }
 
 // ---- backward ----------------------------------------------------------------
-template <typename A, typename T, int TPR, int NV, int VEC>
-__global__ void __launch_bounds__(wg_threads(TPR))
+// The next row's values are fetched while the present one's are worked on.
+template <typename A, typename T, int TPR, int NV, int VEC, bool GATE>
+__global__ void __launch_bounds__(wg_threads(TPR), TPR <= 64 && NV == 1 ? 4 : 1)
 gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_exps,
                          const A* __restrict__ z, const uint8_t* __restrict__ z_exps,
                          const float* __restrict__ w, const float* __restrict__ b,
@@ -240,55 +324,82 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
                          int64_t dy_stride, int64_t dx_stride, int64_t dz_stride)
 {
     constexpr int RPW = wg_threads(TPR) / TPR;     // rows a workgroup takes at a time
-    constexpr int N = NV * VEC;
+    constexpr int N = NV * VEC, NG = GATE ? N : 1, NR = GATE ? NV : 1;
     constexpr bool codes = sizeof(A) == 1;
     __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
     __shared__ float sums[RPW > 1 ? kThreads * N : 1];
     const int l = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+    const int step = (int)gridDim.x * RPW, dt = step / s.H, dh = step - dt * s.H;
 
-    float wv[N], bv[N], dw[N], db[N];
+    float wv[N], bv[NG], dw[N], db[N];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = (i * TPR + l) * VEC;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) wv[i * VEC + e] = bv[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f;
+        for (int e = 0; e < VEC; ++e) {
+            wv[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f;
+            if constexpr (GATE) bv[i * VEC + e] = 0.f;
+        }
         if (j < s.d) {
             load_vec<VEC>(w + j, wv + i * VEC);
-            if (b) load_vec<VEC>(b + j, bv + i * VEC);
+            if constexpr (GATE)
+                if (b) load_vec<VEC>(b + j, bv + i * VEC);
         }
     }
 
-    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += (int64_t)gridDim.x * RPW) {
-        const int64_t row = base + rg;
-        const bool live = row < s.rows;
-        float xv[N], zv[N], gv[N];
-        const A* px = x + (live ? row_at(row, s, x_stride) : 0);
-        const A* pz = z ? z + (live ? row_at(row, s, z_stride) : 0) : nullptr;
-        const T* pd = dy + (live ? row_at(row, s, dy_stride) : 0);
+    struct Row {
+        RawVec<VEC, A> x[NV], z[NR];
+        RawVec<VEC, T> g[NV];
+        uint8_t ex[NV], ez[NR];
+    } next;
+    Place p((int64_t)blockIdx.x * RPW + rg, s);
+    auto fetch = [&]() {
+        const bool live = p.row < s.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * TPR + l) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) xv[i * VEC + e] = zv[i * VEC + e] = gv[i * VEC + e] = 0.f;
+            next.x[i].zero();
+            if constexpr (GATE) next.z[i].zero();
+            next.g[i].zero();
+            next.ex[i] = 127;
+            if constexpr (GATE) next.ez[i] = 127;
             if (live && j < s.d) {
-                load_vec<VEC>(px + j, xv + i * VEC);
-                if (pz) load_vec<VEC>(pz + j, zv + i * VEC);
-                load_vec<VEC>(pd + j, gv + i * VEC);
+                next.x[i].load(x + p.at(x_stride, s) + j);
+                if constexpr (GATE) next.z[i].load(z + p.at(z_stride, s) + j);
+                next.g[i].load(dy + p.at(dy_stride, s) + j);
                 if constexpr (codes) {
-                    const float sx = ckpt_scale(x_exps[row * s.ng + (j >> 7)]);
-                    const float sz = pz ? ckpt_scale(z_exps[row * s.ng + (j >> 7)]) : 0.f;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        xv[i * VEC + e] *= sx;
-                        if (pz) zv[i * VEC + e] *= sz;
-                    }
+                    next.ex[i] = x_exps[p.row * s.ng + (j >> 7)];
+                    if constexpr (GATE) next.ez[i] = z_exps[p.row * s.ng + (j >> 7)];
                 }
             }
         }
+    };
+    fetch();
+    for (int64_t base = (int64_t)blockIdx.x * RPW; base < s.rows; base += step) {
+        const Place at = p;
+        const bool live = at.row < s.rows;
+        float xv[N], zv[NG], gv[N];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            next.x[i].widen(xv + i * VEC);
+            if constexpr (GATE) next.z[i].widen(zv + i * VEC);
+            next.g[i].widen(gv + i * VEC);
+            if constexpr (codes) {
+                const float sx = ckpt_scale(next.ex[i]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[i * VEC + e] *= sx;
+                if constexpr (GATE) {
+                    const float sz = ckpt_scale(next.ez[i]);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) zv[i * VEC + e] *= sz;
+                }
+            }
+        }
+        p.move(step, dt, dh, s);
+        fetch();
         float r = normalise<TPR, NV, VEC>(xv, s, l, red);
         if (!live) r = 0.f;    // a dead row adds nothing to the sums, whatever eps is
         float dot = 0.f, sum = 0.f;
-        T* pdz = dz && live ? dz + row_at(row, s, dz_stride) : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * TPR + l) * VEC;
@@ -298,23 +409,34 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
                 const int c = i * VEC + e;
                 const float n = xv[c] * r;
                 xv[c] = n;
-                if (pz) {
-                    const float zz = zv[c], sg = sigmoid(zz), d = gv[c];
-                    gv[c] = d * (zz * sg);
-                    o[e] = d * fmaf(n, wv[c], bv[c]) * (sg * (1.0f + zz * (1.0f - sg)));
+                if constexpr (GATE) {
+                    // silu' = s + z s (1 - s) = s + silu - silu s
+                    const float sg = sigmoid(zv[c]), d = gv[c], si = zv[c] * sg;
+                    gv[c] = d * si;
+                    o[e] = d * fmaf(n, wv[c], bv[c]) * fmaf(-si, sg, sg + si);
                 }
                 dw[c] = fmaf(gv[c], n, dw[c]);
-                db[c] += gv[c];
-                gv[c] *= wv[c];            // dn
-                dot = fmaf(gv[c], n, dot);
-                sum += gv[c];
             }
-            if (pdz && j < s.d) store_vec<VEC>(pdz + j, o);
+            if constexpr (GATE)
+                if (live && j < s.d) store_vec<VEC>(dz + at.at(dz_stride, s) + j, o);
+        }
+        if (b) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) db[c] += gv[c];
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            gv[c] *= wv[c];            // dn
+            dot = fmaf(gv[c], xv[c], dot);
+        }
+        if (s.center) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) sum += gv[c];
+            sum = row_sum<TPR>(sum, red, 3) * s.inv_d;
         }
         dot = row_sum<TPR>(dot, red, 2) * s.inv_d;
-        sum = s.center ? row_sum<TPR>(sum, red, 3) * s.inv_d : 0.f;
         if (live) {
-            T* pdx = dx + row_at(row, s, dx_stride);
+            T* pdx = dx + at.at(dx_stride, s);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int j = (i * TPR + l) * VEC;
@@ -333,6 +455,7 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
     // this workgroup's partial row of dw, then of db
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+        if (half && !b) break;
         float* a = half ? db : dw;
         if constexpr (RPW > 1) {
             __syncthreads();
@@ -349,41 +472,43 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
             }
         }
         if (rg == 0) {
-            float* p = part + ((int64_t)blockIdx.x * 2 + half) * s.d;
+            float* q = part + ((int64_t)half * gridDim.x + blockIdx.x) * s.d;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int j = (i * TPR + l) * VEC;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (j + e < s.d) p[j + e] = a[i * VEC + e];
+                if (j < s.d) store_vec<VEC>(q + j, a + i * VEC);
             }
         }
     }
 }
 
-// Sums of the partial rows, in a fixed order: 8 columns a workgroup, 32 threads
-// a column, four partial rows in flight each.  parts == 0 writes zeros.
+// Sums of the partial rows, in a fixed order: COLS columns a workgroup, 256 /
+// COLS threads a column, four partial rows in flight each.  parts == 0 writes
+// zeros.  Eight columns spread a narrow row over more workgroups; 32 read whole
+// 128-byte lines of a wide one (d = 5120, 390 parts: 15.7 us with eight).
+template <int COLS>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_weight_kernel(const float* __restrict__ part, int parts, int d, float* __restrict__ dw,
                        float* __restrict__ db)
 {
-    __shared__ float sums[32][9];
-    const int c = threadIdx.x & 7, k = threadIdx.x >> 3;
-    const int j = blockIdx.x * 8 + c, half = blockIdx.y;
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int K = kThreads / COLS;
+    __shared__ float sums[K][COLS + 1];
+    const int c = threadIdx.x % COLS, k = threadIdx.x / COLS;
+    const int j = blockIdx.x * COLS + c, half = blockIdx.y;
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (j < d) {
-        const float* p = part + (int64_t)half * d + j;
+        const float* p = part + (int64_t)half * parts * d + j;
         int i = k;
-        for (; i + 96 < parts; i += 128)
+        for (; i + 7 * K < parts; i += 8 * K)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) a[u] += p[(int64_t)(i + 32 * u) * 2 * d];
-        for (; i < parts; i += 32) a[0] += p[(int64_t)i * 2 * d];
+            for (int u = 0; u < 8; ++u) a[u] += p[(int64_t)(i + K * u) * d];
+        for (; i < parts; i += K) a[0] += p[(int64_t)i * d];
     }
-    sums[k][c] = (a[0] + a[1]) + (a[2] + a[3]);
+    sums[k][c] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
     __syncthreads();
     if (k == 0 && j < d) {
         float t = 0.f;
-        for (int i = 0; i < 32; ++i) t += sums[i][c];
+        for (int i = 0; i < K; ++i) t += sums[i][c];
         (half ? db : dw)[j] = t;
     }
 }
@@ -400,14 +525,17 @@ Choice choose(int d, bool vec8)
         if (d <= 128) return {16, 1, 8};
         if (d <= 256) return {32, 1, 8};
         if (d <= 512) return {64, 1, 8};
+        if (d <= 1024) return {64, 2, 8};
         if (d <= 2048) return {256, 1, 8};
-        if (d <= 4096) return {512, 1, 8};
-        return {1024, 1, 8};
+        if (d <= 4096) return {256, 2, 8};
+        if (d <= 6144) return {256, 3, 8};
+        return {256, 4, 8};
     }
     if (d <= 64) return {64, 1, 1};
     if (d <= 128) return {64, 2, 1};
     if (d <= 256) return {64, 4, 1};
     if (d <= 1024) return {256, 4, 1};
+    if (d <= 2048) return {256, 8, 1};
     if (d <= 4096) return {1024, 4, 1};
     return {1024, 8, 1};
 }
@@ -433,10 +561,12 @@ bool backward_vec8(const NormArgs& a)
 // small next to the data.
 int backward_parts(int64_t rows, int d)
 {
-    const int most = d <= 512 ? 1024 : 512;
+    const int64_t most = d <= 1024 ? 1024 : 512;
     const int tpr = choose(d, true).tpr, rpw = wg_threads(tpr) / tpr;
     const int64_t need = (rows + rpw - 1) / rpw;
-    return (int)(need < most ? need : most);
+    if (need <= most) return (int)need;
+    const int64_t each = (need + most - 1) / most;   // turns a workgroup takes, the same for all but the last
+    return (int)((need + each - 1) / each);
 }
 // Workgroups of the forward pass: one row a row group, more by grid stride.
 unsigned forward_grid(int64_t rows, int tpr)
@@ -453,38 +583,52 @@ Shape shape_of(const NormArgs& a)
 }
 
 #define GDN_NORM_CHOICES(X)                                                                  \
-    X(4, 1, 8) X(8, 1, 8) X(16, 1, 8) X(32, 1, 8) X(64, 1, 8) X(256, 1, 8) X(512, 1, 8)      \
-    X(1024, 1, 8) X(64, 1, 1) X(64, 2, 1) X(64, 4, 1) X(256, 4, 1) X(1024, 4, 1) X(1024, 8, 1)
+    X(4, 1, 8) X(8, 1, 8) X(16, 1, 8) X(32, 1, 8) X(64, 1, 8) X(64, 2, 8) X(256, 1, 8)       \
+    X(256, 2, 8) X(256, 3, 8) X(256, 4, 8) X(64, 1, 1) X(64, 2, 1) X(64, 4, 1) X(256, 4, 1)  \
+    X(256, 8, 1) X(1024, 4, 1) X(1024, 8, 1)
 
-template <typename T>
-void forward_typed(const NormArgs& a, bool vec8, hipStream_t s)
+template <typename T, bool GATE>
+void forward_gated(const NormArgs& a, bool vec8, hipStream_t s)
 {
     const Choice c = choose(a.d, vec8);
     const Shape sh = shape_of(a);
     const dim3 grid(forward_grid(sh.rows, c.tpr));
 #define GDN_RUN(TPR, NV, VEC)                                                                             \
     if (c.tpr == TPR && c.nv == NV && c.vec == VEC)                                                       \
-        hipLaunchKernelGGL((gdn_norm_forward_kernel<T, TPR, NV, VEC>), grid, dim3(wg_threads(TPR)), 0, s,        \
+        hipLaunchKernelGGL((gdn_norm_forward_kernel<T, TPR, NV, VEC, GATE>), grid, dim3(wg_threads(TPR)), 0, s,        \
                            (const T*)a.x, (const T*)a.z, a.w, a.b, (T*)a.y, a.x_codes, a.x_exps_out,      \
                            a.z_codes, a.z_exps_out, sh, a.x_stride, a.z_stride, a.y_stride);
     GDN_NORM_CHOICES(GDN_RUN)
 #undef GDN_RUN
 }
 
-template <typename A, typename T>
-void backward_typed(const NormArgs& a, hipStream_t s)
+template <typename A, typename T, bool GATE>
+void backward_gated(const NormArgs& a, hipStream_t s)
 {
     const Choice c = choose(a.d, backward_vec8(a));
     const Shape sh = shape_of(a);
     const dim3 grid((unsigned)backward_parts(sh.rows, a.d));
 #define GDN_RUN(TPR, NV, VEC)                                                                              \
     if (c.tpr == TPR && c.nv == NV && c.vec == VEC)                                                        \
-        hipLaunchKernelGGL((gdn_norm_backward_kernel<A, T, TPR, NV, VEC>), grid, dim3(wg_threads(TPR)), 0, s,     \
+        hipLaunchKernelGGL((gdn_norm_backward_kernel<A, T, TPR, NV, VEC, GATE>), grid, dim3(wg_threads(TPR)), 0, s,     \
                            (const A*)a.x, a.x_exps, (const A*)a.z, a.z_exps, a.w, a.b, (const T*)a.dy,     \
                            (T*)a.dx, (T*)a.dz, (float*)a.workspace, sh, a.x_stride, a.z_stride,            \
                            a.y_stride, a.dx_stride, a.dz_stride);
     GDN_NORM_CHOICES(GDN_RUN)
 #undef GDN_RUN
+}
+
+template <typename T>
+void forward_typed(const NormArgs& a, bool vec8, hipStream_t s)
+{
+    if (a.z) forward_gated<T, true>(a, vec8, s);
+    else forward_gated<T, false>(a, vec8, s);
+}
+template <typename A, typename T>
+void backward_typed(const NormArgs& a, hipStream_t s)
+{
+    if (a.z) backward_gated<A, T, true>(a, s);
+    else backward_gated<A, T, false>(a, s);
 }
 
 }  // namespace
@@ -550,9 +694,14 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(gdn_norm_weight_kernel, dim3((a.d + 7) / 8, a.db ? 2 : 1), dim3(kThreads), 0, s,
-                       (const float*)a.workspace, a.T > 0 ? backward_parts((int64_t)a.T * a.H, a.d) : 0, a.d,
-                       a.dw, a.db);
+    const int parts = a.T > 0 ? backward_parts((int64_t)a.T * a.H, a.d) : 0;
+    const unsigned halves = a.db ? 2 : 1;
+    if (a.d <= 1024)
+        hipLaunchKernelGGL((gdn_norm_weight_kernel<8>), dim3((a.d + 7) / 8, halves), dim3(kThreads), 0, s,
+                           (const float*)a.workspace, parts, a.d, a.dw, a.db);
+    else
+        hipLaunchKernelGGL((gdn_norm_weight_kernel<32>), dim3((a.d + 31) / 32, halves), dim3(kThreads), 0, s,
+                           (const float*)a.workspace, parts, a.d, a.dw, a.db);
     return hipGetLastError();
 }
 

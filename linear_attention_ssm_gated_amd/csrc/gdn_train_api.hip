@@ -58,6 +58,8 @@ int check_norm(const gdn::NormArgs& a, bool backward)
     }
     if (!a.workspace || a.workspace_bytes < gdn::norm_workspace_bytes(a.T, a.H, a.d))
         return refuse_call(GDN_ERR_WORKSPACE, who, "workspace smaller than gdn_norm_workspace_bytes()");
+    if (reinterpret_cast<uintptr_t>(a.workspace) % 16 != 0)
+        return refuse_call(GDN_ERR_WORKSPACE, who, "workspace must be 16-byte aligned");
     return GDN_OK;
 }
 
