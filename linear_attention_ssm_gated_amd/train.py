@@ -51,41 +51,55 @@ def _lib():
     return _bound
 
 
+# The current stream's handle without a Stream object where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _Call:
     """Pointers of one call's tensors, which must all be on one GPU."""
     __slots__ = ("device",)
 
-    def __init__(self):
-        self.device = -1
+    def __init__(self, first):
+        self.device = first.get_device()
+        if self.device < 0:
+            raise ValueError("tensors must live on the GPU")
 
     def ptr(self, t, dtype=None):
+        """A tensor whose values along the last dimension are contiguous."""
         if t is None:
             return None
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU")
-        if dtype is not None and t.dtype != dtype:
+        if t.get_device() != self.device:
+            raise ValueError("tensors of one call must live on one GPU")
+        if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"expected {dtype}, got {t.dtype}")
-        if t.stride() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("a tensor's last dimension must be contiguous")
-        dev = t.get_device()
-        if self.device != dev:
-            if self.device >= 0:
-                raise ValueError("tensors of one call must be on one GPU")
-            self.device = dev
         return t.data_ptr()
 
     def dense(self, t, dtype=None):
-        if t is not None and not t.is_contiguous():
+        if t is None:
+            return None
+        if t.get_device() != self.device:
+            raise ValueError("tensors of one call must live on one GPU")
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"expected {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        return self.ptr(t, dtype)
+        return t.data_ptr()
 
     def run(self, fn, args, stream):
-        if self.device < 0 or self.device == torch.cuda.current_device():
-            _gdn._check(fn(*args, _gdn._stream(stream)))
+        dev = self.device
+        if dev == torch.cuda.current_device():
+            if stream is None and _raw_stream is not None:
+                status = fn(*args, _raw_stream(dev))
+            else:
+                status = fn(*args, _gdn._stream(stream))
         else:
-            with torch.cuda.device(self.device):
-                _gdn._check(fn(*args, _gdn._stream(stream)))
-        return _gdn.last_route()
+            with torch.cuda.device(dev):
+                status = fn(*args, _gdn._stream(stream))
+        if status != 0:
+            raise _gdn.GdnError(status, _gdn.last_route())
+        return _bound.gdn_last_route().decode()
 
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1}
@@ -110,14 +124,14 @@ def _bytes(t):
 
 def gdn_ckpt8_store(x, codes, exps, rows, d, x_stride, stream=None):
     """Enqueue one 8-bit checkpoint of x [rows][x_stride].  Returns the route line."""
-    c = _Call()
+    c = _Call(x)
     args = (c.ptr(x), c.dense(codes), c.dense(exps, torch.uint8), rows, d, x_stride, _code(x))
     return c.run(_lib().gdn_ckpt8_store, args, stream)
 
 
 def gdn_ckpt8_load(codes, exps, y, rows, d, y_stride, stream=None):
     """Enqueue the reading back of one 8-bit checkpoint.  Returns the route line."""
-    c = _Call()
+    c = _Call(y)
     args = (c.dense(codes), c.dense(exps, torch.uint8), c.ptr(y), rows, d, y_stride, _code(y))
     return c.run(_lib().gdn_ckpt8_load, args, stream)
 
@@ -131,7 +145,7 @@ def gdn_norm_forward(x, z, w, b, y, x_codes, x_exps, z_codes, z_exps, T, H, d, x
     """Enqueue one norm (layouts in include/gdn_train.h).  Returns the route line."""
     if y.dtype != x.dtype or (z is not None and z.dtype != x.dtype):
         raise TypeError("x, z and y must have one dtype")
-    c = _Call()
+    c = _Call(x)
     u8, f32 = torch.uint8, torch.float32
     args = (c.ptr(x), c.ptr(z), c.dense(w, f32), c.dense(b, f32), c.ptr(y), c.dense(x_codes),
             c.dense(x_exps, u8), c.dense(z_codes), c.dense(z_exps, u8), T, H, d, x_stride, z_stride, y_stride,
@@ -149,7 +163,7 @@ def gdn_norm_backward(x, x_exps, z, z_exps, w, b, dy, dx, dz, dw, db, T, H, d, x
     act = GDN_E4M3 if _is_codes(x) else _code(x)
     if z is not None and (GDN_E4M3 if _is_codes(z) else _code(z)) != act:
         raise TypeError("x and z must have one dtype")
-    c = _Call()
+    c = _Call(dy)
     u8, f32 = torch.uint8, torch.float32
     args = (c.ptr(x), c.dense(x_exps, u8), c.ptr(z), c.dense(z_exps, u8), c.dense(w, f32), c.dense(b, f32),
             c.ptr(dy), c.ptr(dx), c.ptr(dz), c.dense(dw, f32), c.dense(db, f32), T, H, d, x_stride, z_stride,
@@ -175,7 +189,7 @@ def gdn_chunk_backward(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, d
     for t in (dq, dk_out, dv_out, dlog_g, dbeta):
         if t.dtype != dout.dtype:
             raise TypeError("dout, dq, dk, dv, dlog_g and dbeta must have one dtype")
-    c = _Call()
+    c = _Call(dout)
     u8, f32 = torch.uint8, torch.float32
     p = c.dense
     args = (p(q), p(k), p(v), p(q_exps, u8), p(k_exps, u8), p(v_exps, u8), p(log_g, f32), p(beta, f32),
