@@ -116,6 +116,84 @@ inline int64_t max_chunks(int B, int T, bool packed)
     return packed ? (int64_t)T / C + B : (int64_t)B * ((T + C - 1) / C);
 }
 
+// T = (I + B diag(beta))^-1 in fp32, by 16 x 16 blocks, 256 threads.  B's lower
+// part is in LDS at sB (pitch kBP floats), sD takes the diagonal blocks (4 x 16 x
+// 17 floats).  solve_diagonal is one wave's: lane (g, n) forms column n of block g
+// by forward substitution.  After a barrier solve_column gives wave w the blocks
+// T_iw as accumulators (rows 16 i + 4 g + s of column 16 w + n, zero above the
+// diagonal): T_iw = -T_ii sum_{m = w}^{i-1} B_im beta_m T_mw on fp32 MFMA
+// (16x16x4), k of step s being 4 g + s, so that an accumulator is the next
+// product's right operand as it is.
+constexpr int kBP = 68;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void solve_diagonal(const float* sB, const float* sBt, float* sD)
+{
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const float* blk = sB + (16 * g) * kBP + 16 * g;
+    f32x4 br[16][4], bt[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) bt[m] = *reinterpret_cast<const f32x4*>(sBt + 16 * g + 4 * m);
+#pragma unroll
+    for (int r = 1; r < 16; ++r)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if (4 * m < r) br[r][m] = *reinterpret_cast<const f32x4*>(blk + r * kBP + 4 * m);
+    __builtin_amdgcn_sched_barrier(0);
+    float t[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) t[r] = r == n ? 1.f : 0.f;
+#pragma unroll
+    for (int m = 0; m < 15; ++m) {
+        const float f = bt[m >> 2][m & 3] * t[m];
+#pragma unroll
+        for (int r = m + 1; r < 16; ++r) t[r] = fmaf(-br[r][m >> 2][m & 3], f, t[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sD[(16 * g + r) * 17 + n] = t[r];
+}
+
+__device__ __forceinline__ void solve_column(const float* sB, const float* sBt, const float* sD, int w, f32x4 (&Tc)[4])
+{
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Tc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i == w) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) Tc[i][s] = sD[(16 * i + 4 * g + s) * 17 + n];
+        } else if (i > w) {
+            f32x4 M = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                if (m >= w) {
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(sB + (16 * i + n) * kBP + 16 * m + 4 * g);
+                    const f32x4 bt = *reinterpret_cast<const f32x4*>(sBt + 16 * m + 4 * g);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) M = mfma4(b[s] * bt[s], Tc[m][s], M);
+                }
+            f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) t = mfma4(sD[(16 * i + n) * 17 + 4 * g + s], M[s], t);
+            Tc[i] = -t;
+        }
+    }
+}
+
+// A workgroup barrier that orders LDS alone: __syncthreads would also wait for
+// every global load and store in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 inline size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace bwd

@@ -37,7 +37,7 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+using bwd::f32x4;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -47,10 +47,6 @@ __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                    c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 __device__ __forceinline__ uint32_t pair(float lo, float hi)
@@ -172,15 +168,7 @@ template <int ROW> __device__ __forceinline__ s16x8 down(const Lane& l, int m, i
 {
     return join(col4<ROW>(l, m, j, 0, t), col4<ROW>(l, m, j, 1, t));
 }
-// A workgroup barrier that orders LDS alone: __syncthreads would also wait for
-// every global load and store in flight.
-__device__ __forceinline__ void lds_barrier()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
+using bwd::lds_barrier;
 // Nothing is moved across: a batch of operand reads is issued whole ahead of the
 // products of the batch before, not one by one in front of each product.
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
@@ -306,7 +294,7 @@ __device__ __forceinline__ float wave_scan(float x, int lane)
 extern __shared__ __attribute__((aligned(1024))) byte lds[];
 
 // ---- prep ------------------------------------------------------------------------
-constexpr int kBP = 68;                        // pitch of the fp32 matrix B
+using bwd::kBP;                                // pitch of the fp32 matrix B
 constexpr int P_K = 0;                         // K
 constexpr int P_Q = P_K + kTile;               // Q, then V
 constexpr int P_B = P_Q + kTile;               // B (fp32), then T^T and (T ga)^T
@@ -414,62 +402,15 @@ gdn_bwd_prep_kernel(Args a)
         }
     }
     lds_barrier();
-    // V takes Q's place; the diagonal blocks of T = (I + B diag(beta))^-1: lane
-    // (g, n) of wave 0 forms column n of block g by forward substitution
+    // V takes Q's place; T = (I + B diag(beta))^-1
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         *reinterpret_cast<u32x4*>(sQ + staged<256>(tid, i)) = vr[i].bits();
     }
-    if (w == 0) {
-        const float* blk = sB + (16 * g) * kBP + 16 * g;
-        f32x4 br[16][4], bt[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) bt[m] = *reinterpret_cast<const f32x4*>(sBt + 16 * g + 4 * m);
-#pragma unroll
-        for (int r = 1; r < 16; ++r)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                if (4 * m < r) br[r][m] = *reinterpret_cast<const f32x4*>(blk + r * kBP + 4 * m);
-        sched_fence();
-        float t[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) t[r] = r == n ? 1.f : 0.f;
-#pragma unroll
-        for (int m = 0; m < 15; ++m) {
-            const float f = bt[m >> 2][m & 3] * t[m];
-#pragma unroll
-            for (int r = m + 1; r < 16; ++r) t[r] = fmaf(-br[r][m >> 2][m & 3], f, t[r]);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sD[(16 * g + r) * 17 + n] = t[r];
-    }
+    if (w == 0) bwd::solve_diagonal(sB, sBt, sD);
     lds_barrier();
-    // column block w: T_iw = -T_ii sum_{m = w}^{i-1} B_im beta_m T_mw in fp32
-    // products, k of step s being 4g + s, so that an accumulator is the next
-    // product's right operand as it is
     f32x4 Tc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        Tc[i] = zero4();
-        if (i == w) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) Tc[i][s] = sD[(16 * i + 4 * g + s) * 17 + n];
-        } else if (i > w) {
-            f32x4 M = zero4();
-#pragma unroll
-            for (int m = 0; m < i; ++m)
-                if (m >= w) {
-                    const f32x4 b = *reinterpret_cast<const f32x4*>(sB + (16 * i + n) * kBP + 16 * m + 4 * g);
-                    const f32x4 bt = *reinterpret_cast<const f32x4*>(sBt + 16 * m + 4 * g);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) M = mfma4(b[s] * bt[s], Tc[m][s], M);
-                }
-            f32x4 t = zero4();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) t = mfma4(sD[(16 * i + n) * 17 + 4 * g + s], M[s], t);
-            Tc[i] = -t;
-        }
-    }
+    bwd::solve_column(sB, sBt, sD, w, Tc);
     lds_barrier();   // every read of B is done
     {
         const int c = 16 * w + n;
