@@ -773,12 +773,6 @@ size_t grads_lds(const Sizes& s)
 }
 int slices_of(const Sizes& s) { return (s.dvp + kCols - 1) / kCols; }
 
-template <typename K>
-hipError_t allow_lds(K kernel, size_t bytes)
-{
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 // The head sizes' tile counts, 2, 4 or 8 each, as compile-time constants.
 template <typename F>
 hipError_t with_tiles(int n, F&& f)
@@ -791,8 +785,7 @@ hipError_t with_tiles(int n, F&& f)
 template <typename K>
 hipError_t run(K kernel, dim3 grid, size_t lds, hipStream_t s, const Args& k)
 {
-    // per call: an attribute of the kernel on the current device
-    const hipError_t e = lds > 0 ? allow_lds(kernel, lds) : hipSuccess;
+    const hipError_t e = lds > 0 ? allow_lds(reinterpret_cast<const void*>(kernel), lds) : hipSuccess;
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), lds, s, k);
     return hipGetLastError();

@@ -1188,19 +1188,13 @@ Layout layout(int B, int T, int Hv, bool packed)
     return l;
 }
 
-template <typename K>
-hipError_t allow_lds(K kernel, int bytes)
-{
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename TA>
 hipError_t launch_typed(const Args& k, int64_t chunks, hipStream_t s)
 {
     hipError_t e;
-    if ((e = allow_lds(gdn_bwd_prep_kernel<TA>, kPrepLds)) != hipSuccess) return e;
-    if ((e = allow_lds(gdn_bwd_spine_kernel<TA>, kSpineLds)) != hipSuccess) return e;
-    if ((e = allow_lds(gdn_bwd_grads_kernel<TA>, kGradLds)) != hipSuccess) return e;
+    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_prep_kernel<TA>), kPrepLds)) != hipSuccess) return e;
+    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_spine_kernel<TA>), kSpineLds)) != hipSuccess) return e;
+    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_grads_kernel<TA>), kGradLds)) != hipSuccess) return e;
     if (k.cu) hipLaunchKernelGGL(gdn_bwd_table_kernel, dim3(1), dim3(256), 0, s, k.cu, k.B, k.T, k.base);
     if (chunks > 0)
         hipLaunchKernelGGL((gdn_bwd_prep_kernel<TA>), dim3((unsigned)chunks, k.Hv), dim3(256), kPrepLds, s, k);

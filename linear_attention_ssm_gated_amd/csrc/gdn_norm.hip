@@ -154,6 +154,31 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red,
     return x;
 }
 
+// two sums at once, in slots slot and slot + 1
+template <int TPR> __device__ __forceinline__ void row_sum2(float& x, float& y, float* red, int slot)
+{
+    constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) {
+        x += __shfl_xor(x, o);
+        y += __shfl_xor(y, o);
+    }
+    if constexpr (TPR > 64) {
+        float *r = red + slot * kMaxWaves, *t = r + kMaxWaves;
+        if ((threadIdx.x & 63) == 0) {
+            r[threadIdx.x >> 6] = x;
+            t[threadIdx.x >> 6] = y;
+        }
+        __syncthreads();
+        x = y = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) {
+            x += r[i];
+            y += t[i];
+        }
+    }
+}
+
 // The hardware's exp2 and reciprocal, within one unit in the last place each: a
 // relative error of a few 2^-24, where the correctly rounded division alone
 // took ten instructions of the thirty-five that a gated value needs in all.
@@ -194,26 +219,41 @@ struct Place {
     __device__ __forceinline__ int64_t at(int64_t stride, const Shape& s) const { return (int64_t)t * stride + h * s.d; }
 };
 
-// The row's values minus their mean (center), and 1 / sqrt(var + eps).
+// The row's values minus their mean (center), and 1 / sqrt(var + eps).  The
+// mean of a row far from zero is known to 2^-24 of itself only; what is left of
+// it in the differences, which lose nothing, is taken out with the sum that the
+// variance's pass forms beside the squares (a row of 1000 +- 0.7: 4e-5 of y
+// without it, 1e-7 with).
 template <int TPR, int NV, int VEC>
 __device__ __forceinline__ float normalise(float* x, const Shape& s, int l, float* red)
 {
-    if (s.center) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < NV * VEC; ++e) m += x[e];
-        m = row_sum<TPR>(m, red, 0) * s.inv_d;
+    auto minus = [&](float m) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if ((i * TPR + l) * VEC < s.d)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) x[i * VEC + e] -= m;
+    };
+    if (s.center) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < NV * VEC; ++e) m += x[e];
+        minus(row_sum<TPR>(m, red, 0) * s.inv_d);
     }
-    float q = 0.f;
+    float q = 0.f, c = 0.f;
 #pragma unroll
     for (int e = 0; e < NV * VEC; ++e) q = fmaf(x[e], x[e], q);
-    q = row_sum<TPR>(q, red, 1) * s.inv_d;
-    return __builtin_amdgcn_rsqf(q + s.eps);
+    if (s.center) {
+#pragma unroll
+        for (int e = 0; e < NV * VEC; ++e) c += x[e];
+        row_sum2<TPR>(q, c, red, 1);
+        c *= s.inv_d;
+        minus(c);
+        q = fmaf(-c, c, q * s.inv_d);
+    } else {
+        q = row_sum<TPR>(q, red, 1) * s.inv_d;
+    }
+    return __builtin_amdgcn_rsqf(fmaxf(q, 0.f) + s.eps);
 }
 
 // Codes and scale byte of the VEC = 8 values of each lane, a group's 128 lying
@@ -254,7 +294,7 @@ gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const 
                         uint8_t* __restrict__ z_exps, Shape s, int64_t x_stride, int64_t z_stride,
                         int64_t y_stride)
 {
-    __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
+    __shared__ float red[TPR > 64 ? 6 * kMaxWaves : 1];
     constexpr int RPW = wg_threads(TPR) / TPR;
     const int l = threadIdx.x % TPR;
     const int step = (int)gridDim.x * RPW, dt = step / s.H, dh = step - dt * s.H;
@@ -286,7 +326,7 @@ gdn_norm_forward_kernel(const T* __restrict__ x, const T* __restrict__ z, const 
         }
         // LDS slots by turns: an RMS norm's one reduction a row would let the
         // next row's writers overtake this row's readers
-        const float r = normalise<TPR, NV, VEC>(xv, s, l, red + 2 * kMaxWaves * turn);
+        const float r = normalise<TPR, NV, VEC>(xv, s, l, red + 3 * kMaxWaves * turn);
         turn = TPR > 64 ? turn ^ 1 : 0;
         if (!live) continue;
         T* py = y + p.at(y_stride, s);
@@ -326,7 +366,7 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
     constexpr int RPW = wg_threads(TPR) / TPR;     // rows a workgroup takes at a time
     constexpr int N = NV * VEC, NG = GATE ? N : 1, NR = GATE ? NV : 1;
     constexpr bool codes = sizeof(A) == 1;
-    __shared__ float red[TPR > 64 ? 4 * kMaxWaves : 1];
+    __shared__ float red[TPR > 64 ? 6 * kMaxWaves : 1];
     __shared__ float sums[RPW > 1 ? kThreads * N : 1];
     const int l = threadIdx.x % TPR, rg = threadIdx.x / TPR;
     const int step = (int)gridDim.x * RPW, dt = step / s.H, dh = step - dt * s.H;
@@ -432,9 +472,12 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
         if (s.center) {
 #pragma unroll
             for (int c = 0; c < N; ++c) sum += gv[c];
-            sum = row_sum<TPR>(sum, red, 3) * s.inv_d;
+            row_sum2<TPR>(dot, sum, red, 3);
+            sum *= s.inv_d;
+        } else {
+            dot = row_sum<TPR>(dot, red, 3);
         }
-        dot = row_sum<TPR>(dot, red, 2) * s.inv_d;
+        dot *= s.inv_d;
         if (live) {
             T* pdx = dx + at.at(dx_stride, s);
 #pragma unroll
@@ -643,7 +686,7 @@ Geometry norm_forward_geometry(const NormArgs& a)
     const Choice c = choose(a.d, forward_vec8(a));
     return Geometry{c.vec == 8 ? "gdn_norm_forward_kernel<8>" : "gdn_norm_forward_kernel<1>",
                     {forward_grid((int64_t)a.T * a.H, c.tpr), 1, 1}, (unsigned)wg_threads(c.tpr),
-                    c.tpr > 64 ? (unsigned)(4 * kMaxWaves * sizeof(float)) : 4u};
+                    c.tpr > 64 ? (unsigned)(6 * kMaxWaves * sizeof(float)) : 4u};
 }
 
 Geometry norm_backward_geometry(const NormArgs& a)
@@ -652,7 +695,7 @@ Geometry norm_backward_geometry(const NormArgs& a)
     return Geometry{c.vec == 8 ? "gdn_norm_backward_kernel<8>+gdn_norm_weight_kernel"
                                : "gdn_norm_backward_kernel<1>+gdn_norm_weight_kernel",
                     {(unsigned)backward_parts((int64_t)a.T * a.H, a.d), 1, 1}, (unsigned)wg_threads(c.tpr),
-                    (unsigned)(c.tpr > 64 ? 4 * kMaxWaves * sizeof(float)
+                    (unsigned)(c.tpr > 64 ? 6 * kMaxWaves * sizeof(float)
                                           : kThreads * c.nv * c.vec * sizeof(float))};
 }
 

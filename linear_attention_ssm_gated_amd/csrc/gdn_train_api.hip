@@ -5,6 +5,26 @@
 
 #include <math.h>
 
+#include <mutex>
+#include <set>
+#include <utility>
+
+namespace gdn {
+hipError_t allow_lds(const void* kernel, size_t bytes)
+{
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> allowed;
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (allowed.count({dev, kernel})) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) allowed.insert({dev, kernel});
+    return e;
+}
+}  // namespace gdn
+
 namespace {
 
 using gdn::refuse_call;

@@ -80,6 +80,10 @@ hipError_t launch_backward_mfma(const BackwardArgs& a, hipStream_t s);
 Geometry backward_generic_geometry(const BackwardArgs& a);
 hipError_t launch_backward_generic(const BackwardArgs& a, hipStream_t s);
 
+// Lets a kernel take `bytes` of dynamic LDS on the current device (beyond the
+// runtime's default limit); the runtime is asked once per kernel and device.
+hipError_t allow_lds(const void* kernel, size_t bytes);
+
 // Route-line helpers of the C ABI layer (gdn_api.hip): a named refusal, the line
 // of an accepted call, and the status of its launches.
 int refuse_call(int status, const char* who, const char* why);
