@@ -32,6 +32,18 @@ namespace bwd {
 
 constexpr int C = 64;
 
+// Work item of this workgroup.  Workgroups go to the eight XCDs in turn, each
+// with an L2 of its own; numbered like this, neighbouring items (which share
+// rows of k, q and of the workspace) meet in one L2.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int64_t xcd_item()
+{
+    const int64_t n = (int64_t)gridDim.x * gridDim.y * gridDim.z;
+    const int64_t id = blockIdx.x + (int64_t)gridDim.x * (blockIdx.y + (int64_t)gridDim.y * blockIdx.z);
+    const int64_t each = n / kXcds, more = n % kXcds, xcd = id % kXcds;
+    return xcd * each + (xcd < more ? xcd : more) + id / kXcds;
+}
+
 struct ChunkAt {
     int b;          // sequence
     int c;          // chunk within it

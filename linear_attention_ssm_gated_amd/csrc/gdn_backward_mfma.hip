@@ -3,9 +3,7 @@
 // The formulas are in gdn_backward_common.h.  Three kernels:
 //   prep    one workgroup per (chunk, v-head): B, P, T; W, U, Qt
 //   spine   one workgroup per (sequence, v-head, 64 dv columns, direction):
-//           the states forwards and their gradients backwards in one launch;
-//           each wave owns 16 columns, so a step's two products follow each
-//           other in its registers
+//           the states forwards and their gradients backwards in one launch
 //   grads   one workgroup per (chunk, k-head): the gradients of the chunk, the
 //           v-heads of the k-head in turn, dq and dk summed in registers
 //
@@ -312,7 +310,9 @@ __global__ void __launch_bounds__(256, 2)
 gdn_bwd_prep_kernel(Args a)
 {
     ChunkAt at;
-    const int x = blockIdx.x, vh = blockIdx.y, kh = vh / (a.Hv / a.Hk);
+    // the v-heads of a k-head, which share k and q, are neighbours
+    const int64_t item = bwd::xcd_item();
+    const int vh = (int)(item % a.Hv), x = (int)(item / a.Hv), kh = vh / (a.Hv / a.Hk);
     if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, n = lane & 15;
@@ -496,52 +496,68 @@ gdn_bwd_prep_kernel(Args a)
 }
 
 // ---- spine -------------------------------------------------------------------------
+// Eight waves.  Four walk: each owns 16 dv columns of the state, so that a step's
+// two products follow each other in its registers.  Four load: the next chunks'
+// matrices through registers (three steps ahead) into the LDS stage that is not
+// being read, so that a load or an LDS write that waits for the compute unit's
+// memory path holds up no product (loads issued by the walking waves: 2.6 us a
+// step against the products' 0.3).
 // One stage of LDS holds a chunk's matrices: forwards W, K and U's columns,
-// backwards K, W, Qt and do's columns.  The next chunk's rows wait in registers
-// and are written to the other stage while this one is read.
+// backwards K, W, Qt and do's columns.
 constexpr int kCols = 64;
+constexpr int kSpineThreads = 512;
 constexpr int S_L = 0;                     // W, or K
 constexpr int S_R = S_L + kTile;           // K, or W
 constexpr int S_X = S_R + kTile;           // Qt (backwards)
 constexpr int S_C = S_X + kTile;           // U, or do: [64][64]
-constexpr int S_G = S_C + kSquare;          // G_L log2(e)
+constexpr int S_G = S_C + kSquare;         // G_L log2(e)
 constexpr int kStage = S_G + 1024;
 constexpr int kSpineLds = 2 * kStage;
 
+// Where a workgroup walks.
+struct Walk {
+    int vh, kh, half, b, nc;
+    bool rev;
+    int64_t row0, len, x0;
+    __device__ __forceinline__ explicit Walk(const Args& a)
+    {
+        // the halves of a v-head, which read the same W, Qt and K step by step, are
+        // neighbours, then the v-heads of a k-head; the two directions, which meet
+        // only half way, come one after the other; each XCD has all sequences,
+        // whose lengths differ
+        int64_t i = bwd::xcd_item();
+        half = (int)(i & 1);
+        i >>= 1;
+        const int rep = a.Hv / a.Hk;
+        const int g = (int)(i % rep);
+        i /= rep;
+        rev = (i & 1) != 0;
+        i >>= 1;
+        b = (int)(i % a.B);
+        kh = (int)(i / a.B);
+        vh = kh * rep + g;
+        bwd::seq_rows(a.cu, b, a.T, &row0, &len);
+        nc = (int)((len + C - 1) / C);
+        x0 = a.cu ? a.base[b] : (int64_t)b * a.nc_dense;
+    }
+};
+
 template <typename TA, bool REV>
-__device__ __forceinline__ void spine_walk(const Args& a)
+__device__ __forceinline__ void spine_load(const Args& a, const Walk& k)
 {
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, n = lane & 15;
-    const int vh = blockIdx.x >> 1, half = blockIdx.x & 1, b = blockIdx.y, kh = vh / (a.Hv / a.Hk);
-    const int col = half * kCols + 16 * w + n;       // this lane's dv column
-
-    int64_t row0, len;
-    bwd::seq_rows(a.cu, b, a.T, &row0, &len);
-    const int nc = (int)((len + C - 1) / C);
-    const int64_t x0 = a.cu ? a.base[b] : (int64_t)b * a.nc_dense;
-    const float* from = REV ? a.dht : a.h0;
-    const size_t hoff = ((size_t)b * a.Hv + vh) * D * D;
-
-    f32x4 st[8];                                     // dk index sig(t, 4g + s)
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            st[t][s] = from ? from[hoff + (size_t)(sig0(t) + 8 * g + s) * D + col] : 0.f;
-
-    // a chunk's matrices on their way to LDS
+    const int tid = threadIdx.x & 255;
     struct Regs {
         u32x4 W[4], x[4], c[2];
         Raw<TA> K[4];
         float gl;
-    } in0, in1;
+    } in[3];
     auto fetch = [&](Regs& in, int i) {      // the i-th chunk of the walk
-        const int c = REV ? nc - 1 - i : i;
-        const byte* head = a.heads + ((size_t)(x0 + c) * a.Hv + vh) * W_BYTES;
-        const int64_t r0 = row0 + (int64_t)c * C;
-        const int rows = (int)min((int64_t)C, len - (int64_t)c * C);
-        const Rows<TA> rk(a.k, a.k_exps, r0, rows, a.Hk, kh);
+        i = min(i, k.nc - 1);
+        const int c = REV ? k.nc - 1 - i : i;
+        const byte* head = a.heads + ((size_t)(k.x0 + c) * a.Hv + k.vh) * W_BYTES;
+        const int64_t r0 = k.row0 + (int64_t)c * C;
+        const int rows = (int)min((int64_t)C, k.len - (int64_t)c * C);
+        const Rows<TA> rk(a.k, a.k_exps, r0, rows, a.Hk, k.kh);
         const rsrc_t rh = make_rsrc(head, W_BYTES);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -549,114 +565,144 @@ __device__ __forceinline__ void spine_walk(const Args& a)
             if (REV) in.x[j] = load16(rh, 16 * tid, W_QT + 4096 * j);
             in.K[j] = rk.load(tid >> 4, tid & 15, 16 * j);
         }
-        const Rows<uint16_t> ro(a.dout, nullptr, r0, REV ? rows : 0, a.Hv, vh);
+        const Rows<uint16_t> ro(a.dout, nullptr, r0, REV ? rows : 0, a.Hv, k.vh);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = tid >> 3, q = tid & 7;
-            in.c[j] = REV ? ro.load(r, 8 * half + q, 32 * j).v
-                          : load16(rh, r * 256 + 128 * half + 16 * q, W_U + 8192 * j);
+            in.c[j] = REV ? ro.load(r, 8 * k.half + q, 32 * j).v
+                          : load16(rh, r * 256 + 128 * k.half + 16 * q, W_U + 8192 * j);
         }
-        in.gl = reinterpret_cast<const float*>(head + W_G)[C - 1];
+        in.gl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rh, 0, W_G + 4 * (C - 1), 0));
     };
-    auto put = [&](const Regs& in, byte* S) {
+    auto put = [&](const Regs& in, int S) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int o = staged<256>(tid, j);
-            *reinterpret_cast<u32x4*>(S + (REV ? S_R : S_L) + o) = in.W[j];
-            *reinterpret_cast<u32x4*>(S + (REV ? S_L : S_R) + o) = in.K[j].bits();
-            if (REV) *reinterpret_cast<u32x4*>(S + S_X + o) = in.x[j];
+            byte* o = lds + S + staged<256>(tid, j);
+            *reinterpret_cast<u32x4*>(o + (REV ? S_R : S_L)) = in.W[j];
+            *reinterpret_cast<u32x4*>(o + (REV ? S_L : S_R)) = in.K[j].bits();
+            if (REV) *reinterpret_cast<u32x4*>(o + S_X) = in.x[j];
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            *reinterpret_cast<u32x4*>(S + S_C + staged<128>(tid, j)) = in.c[j];
-        }
-        if (tid == 0) *reinterpret_cast<float*>(S + S_G) = in.gl;
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(lds + S + S_C + staged<128>(tid, j)) = in.c[j];
+        *reinterpret_cast<float*>(lds + S + S_G) = in.gl;      // the same value from every thread
     };
-
-    const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
-    if (nc > 0) {
-        fetch(in0, 0);
-        fetch(in1, min(1, nc - 1));
-        put(in0, lds);
+    // chunk i's set is i % 3; past the end the last chunk is fetched again and
+    // written to a stage that nobody reads (no branches)
+    fetch(in[0], 0);
+    fetch(in[1], 1);
+    fetch(in[2], 2);
+    put(in[0], 0);
+    fetch(in[0], 3);
+    lds_barrier();
+    auto step = [&](int i, Regs& r) {
+        put(r, ((i + 1) & 1) * kStage);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(r, i + 4);
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+    };
+    // whole turns of three, so that no path skips a fetch: the compiler's waits,
+    // which count the loads behind the one that is needed, serve every path
+    for (int i = 0; i < k.nc; i += 3) {
+        step(i, in[1]);
+        step(i + 1, in[2]);
+        step(i + 2, in[0]);
     }
+}
+
+template <bool REV>
+__device__ __forceinline__ void spine_step(const Args& a, const Walk& k)
+{
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    const int col = k.half * kCols + 16 * w + n;     // this lane's dv column
+    const float* from = REV ? a.dht : a.h0;
+    const size_t hoff = ((size_t)k.b * a.Hv + k.vh) * D * D;
+
+    f32x4 st[8];                                     // dk index sig(t, 4g + s)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            st[t][s] = from ? from[hoff + (size_t)(sig0(t) + 8 * g + s) * D + col] : 0.f;
     // the start state has arrived: else the loop's waits, which serve its first
-    // pass too, would wait for every load in flight each time
+    // pass too, would wait for the stores in flight each time
 #pragma unroll
     for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(st[t]));
-    if (nc > 0) fetch(in0, min(2, nc - 1));
-    lds_barrier();
-    // Step i reads chunk i from stage i % 2, then writes chunk i + 1 to the other
-    // one and fetches chunk i + 3 into the registers that this leaves free: a
-    // load has two steps to arrive.  Past the end the last chunk is fetched again
-    // and written to a stage that nobody reads (no branches).
-    auto step = [&](int i, Regs& in) {
+    const Lane L((uint32_t)(uintptr_t)(lds_ptr)lds);
+    if (k.nc > 0) lds_barrier();
+    for (int i = 0; i < k.nc; ++i) {
         const int S = (i & 1) * kStage;
-        s16x8 lf[4][4], rf[8][2], xf[8][2], ob[2];
-        s16x4 uf[4];
+        s16x8 lf[4][4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) lf[rt][ks] = row8_sig<256>(L, S + S_L, rt, ks);
+            for (int rt = 0; rt < 4; ++rt) lf[rt][ks] = row8_sig<256>(L, S + S_L, rt, ks);
         const float gl = __builtin_amdgcn_exp2f(*reinterpret_cast<const float*>(lds + S + S_G));
         sched_fence();
-
-        const int c = REV ? nc - 1 - i : i;
-        byte* out = (REV ? a.dh : a.h) + ((size_t)(x0 + c) * a.Hv + vh) * kState + col * 256;
         s16x8 sb[4];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            sb[ks] = frag(st[2 * ks], st[2 * ks + 1]);
-            *reinterpret_cast<s16x8*>(out + 16 * (4 * ks + g)) = sb[ks];
-        }
+        for (int ks = 0; ks < 4; ++ks) sb[ks] = frag(st[2 * ks], st[2 * ks + 1]);
         f32x4 d[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) d[rt] = zero4();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) d[rt] = mfma(lf[rt][ks], sb[ks], d[rt]);
-        // the operands of the second product, while the first one runs
-        if (!REV) {
+        sched_fence();
+        // the second product's operands, half its rows at a time, while the first
+        // product runs
+        s16x8 rf[2][8], xf[2][8], ob[2];
+        s16x4 uf[4];
+        auto read = [&](int j) {
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) uf[rt] = col4<128>(L, S + S_C, rt >> 1, rt & 1, w);
-        } else {
+            for (int t = 0; t < 8; ++t) {
+                if (REV) xf[j][t] = down_sig<256>(L, S + S_X, j, t);
+                rf[j][t] = down_sig<256>(L, S + S_R, j, t);
+            }
+        };
+        if (REV) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) ob[j] = down<128>(L, S + S_C, j, w);
+        } else {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) uf[rt] = col4<128>(L, S + S_C, rt >> 1, rt & 1, w);
         }
+        read(0);
+        sched_fence();
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int ks = 2; ks < 4; ++ks)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (REV) xf[t][j] = down_sig<256>(L, S + S_X, j, t);
-                rf[t][j] = down_sig<256>(L, S + S_R, j, t);
-            }
+            for (int rt = 0; rt < 4; ++rt) d[rt] = mfma(lf[rt][ks], sb[ks], d[rt]);
+        sched_fence();
+        read(1);
+        const int c = REV ? k.nc - 1 - i : i;
+        byte* out = (REV ? a.dh : a.h) + ((size_t)(k.x0 + c) * a.Hv + k.vh) * kState + col * 256;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) *reinterpret_cast<s16x8*>(out + 16 * (4 * ks + g)) = sb[ks];
         sched_fence();
 #pragma unroll
         for (int t = 0; t < 8; ++t) st[t] *= gl;
         if (REV) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int t = 0; t < 8; ++t) st[t] = mfma(xf[t][j], ob[j], st[t]);
+            for (int t = 0; t < 8; ++t) st[t] = mfma(xf[0][t], ob[0], st[t]);
         }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) d[rt] = REV ? -d[rt] : widen(uf[rt]) - d[rt];
         const s16x8 db[2] = {frag(d[0], d[1]), frag(d[2], d[3])};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int t = 0; t < 8; ++t) st[t] = mfma(rf[0][t], db[0], st[t]);
+        if (REV) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t) st[t] = mfma(rf[t][j], db[j], st[t]);
-        sched_fence();
-        put(in, lds + (kStage - S));
-        sched_fence();
-        fetch(in, min(i + 3, nc - 1));
+            for (int t = 0; t < 8; ++t) st[t] = mfma(xf[1][t], ob[1], st[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) st[t] = mfma(rf[1][t], db[1], st[t]);
         sched_fence();
         lds_barrier();
-    };
-    for (int i = 0; i < nc; i += 2) {
-        step(i, in1);
-        if (i + 1 < nc) step(i + 1, in0);
     }
+    for (int i = k.nc; i % 3 != 0; ++i) lds_barrier();   // the loading waves' last turn
     if (REV && a.dh0)
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -665,11 +711,19 @@ __device__ __forceinline__ void spine_walk(const Args& a)
 }
 
 template <typename TA>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kSpineThreads)
 gdn_bwd_spine_kernel(Args a)
 {
-    if (blockIdx.z == 0) spine_walk<TA, false>(a);
-    else spine_walk<TA, true>(a);
+    const Walk k(a);
+    const bool loads = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
+    if (loads) {
+        if (k.nc == 0) return;
+        if (k.rev) spine_load<TA, true>(a, k);
+        else spine_load<TA, false>(a, k);
+    } else {
+        if (k.rev) spine_step<true>(a, k);
+        else spine_step<false>(a, k);
+    }
 }
 
 // ---- grads -------------------------------------------------------------------------
@@ -1198,7 +1252,7 @@ hipError_t launch_typed(const Args& k, int64_t chunks, hipStream_t s)
     if (k.cu) hipLaunchKernelGGL(gdn_bwd_table_kernel, dim3(1), dim3(256), 0, s, k.cu, k.B, k.T, k.base);
     if (chunks > 0)
         hipLaunchKernelGGL((gdn_bwd_prep_kernel<TA>), dim3((unsigned)chunks, k.Hv), dim3(256), kPrepLds, s, k);
-    hipLaunchKernelGGL((gdn_bwd_spine_kernel<TA>), dim3(k.Hv * 2, k.B, 2), dim3(256), kSpineLds, s, k);
+    hipLaunchKernelGGL((gdn_bwd_spine_kernel<TA>), dim3(k.Hv * 2, k.B, 2), dim3(kSpineThreads), kSpineLds, s, k);
     if (chunks > 0)
         hipLaunchKernelGGL((gdn_bwd_grads_kernel<TA>), dim3((unsigned)chunks, k.Hk), dim3(kGradThreads), kGradLds, s, k);
     return hipGetLastError();
@@ -1224,7 +1278,7 @@ size_t backward_mfma_workspace_bytes(const BackwardArgs& a) { return layout(a.B,
 Geometry backward_mfma_geometry(const BackwardArgs& a)
 {
     return Geometry{"gdn_bwd_prep_kernel+gdn_bwd_spine_kernel+gdn_bwd_grads_kernel",
-                    {(unsigned)(a.Hv * 2), (unsigned)a.B, 2}, 256, (unsigned)kSpineLds};
+                    {(unsigned)(a.Hv * 2), (unsigned)a.B, 2}, kSpineThreads, (unsigned)kSpineLds};
 }
 
 hipError_t launch_backward_mfma(const BackwardArgs& a, hipStream_t s)
