@@ -93,6 +93,14 @@ template <int ROW> __device__ __forceinline__ int staged(int tid, int i)
     if constexpr (ROW == 256) return (granule<256>(tid >> 4, tid & 15) ^ (32 * (i & 1))) + 4096 * i;
     else return granule<128>(tid >> 3, tid & 7) + 4096 * i;
 }
+// The same for a matrix that lies in memory as products leave it ("tile order":
+// 1 KiB for 16 rows x 32 columns, lane 16 g + n's eight columns 8 g .. of row n at
+// byte 16 lane, four of these a 16-row tile): whole 1 KiB stores and loads, where
+// rows of 256 bytes took 64 bytes of 16 rows a store.
+__device__ __forceinline__ int staged_tile(int tid, int i)
+{
+    return (granule<256>(tid & 15, tid >> 4) ^ (32 * (i & 1))) + 4096 * i;
+}
 // Operand reads.  A lane's address of an operand differs from tile to tile and
 // k-step to k-step by an exclusive or of constant swizzle bits and a constant
 // offset, so that eight lane bases, one for each way of reading, serve them all.
@@ -239,9 +247,9 @@ template <typename TA> struct Rows {
 };
 
 // Workspace of one (chunk, v-head), in bytes.
-constexpr int W_W = 0;                       // [64][128]
-constexpr int W_QT = W_W + kTile;            // [64][128]
-constexpr int W_U = W_QT + kTile;            // [64][128]
+constexpr int W_W = 0;                       // [64][128] in tile order
+constexpr int W_QT = W_W + kTile;            // likewise
+constexpr int W_U = W_QT + kTile;            // likewise
 constexpr int W_TT = W_U + kTile;            // T^T [64][64]
 constexpr int W_PT = W_TT + kSquare;         // P^T [64][64]
 constexpr int W_B = W_PT + kSquare;          // B's ten lower tiles in accumulator order, 512 bytes each
@@ -260,7 +268,7 @@ struct Args {
     int nc_dense;
     int32_t* base;       // chunk table (packed)
     byte* heads;         // [chunk][Hv] W_BYTES
-    byte* h;             // [chunk][Hv] start states, bf16, transposed: [dv][dk]
+    byte* h;             // [chunk][Hv] start states, bf16, transposed [dv][dk], in tile order
     byte* dh;            // [chunk][Hv] end gradients, likewise
 };
 
@@ -486,7 +494,7 @@ gdn_bwd_prep_kernel(Args a)
                     qq[i] = mfma(kf[i][j], pg[rt & 1][j], qq[i]);
                 }
         const float eb = sEb[r], ga = sGa[r];
-        const int o = r * 256 + 16 * (4 * w + g);
+        const int o = 4096 * rt + 1024 * w + 16 * lane;
         *reinterpret_cast<u32x4*>(out + W_W + o) = pack8(ww[0] * eb, ww[1] * eb);
         *reinterpret_cast<u32x4*>(out + W_U + o) = pack8(uu[0] * eb, uu[1] * eb);
         const s16x8 qb = __builtin_bit_cast(s16x8, q8[rt].bits());
@@ -568,22 +576,25 @@ __device__ __forceinline__ void spine_load(const Args& a, const Walk& k)
         const Rows<uint16_t> ro(a.dout, nullptr, r0, REV ? rows : 0, a.Hv, k.vh);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int r = tid >> 3, q = tid & 7;
-            in.c[j] = REV ? ro.load(r, 8 * k.half + q, 32 * j).v
-                          : load16(rh, r * 256 + 128 * k.half + 16 * q, W_U + 8192 * j);
+            // do: rows; U: the two 1 KiB pieces of this half's columns in two row tiles
+            in.c[j] = REV ? ro.load(tid >> 3, 8 * k.half + (tid & 7), 32 * j).v
+                          : load16(rh, 4096 * (tid >> 7) + 16 * (tid & 127), W_U + 2048 * k.half + 8192 * j);
         }
         in.gl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rh, 0, W_G + 4 * (C - 1), 0));
     };
     auto put = [&](const Regs& in, int S) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            byte* o = lds + S + staged<256>(tid, j);
+            byte* o = lds + S + staged_tile(tid, j);
             *reinterpret_cast<u32x4*>(o + (REV ? S_R : S_L)) = in.W[j];
-            *reinterpret_cast<u32x4*>(o + (REV ? S_L : S_R)) = in.K[j].bits();
             if (REV) *reinterpret_cast<u32x4*>(o + S_X) = in.x[j];
+            *reinterpret_cast<u32x4*>(lds + S + staged<256>(tid, j) + (REV ? S_L : S_R)) = in.K[j].bits();
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(lds + S + S_C + staged<128>(tid, j)) = in.c[j];
+        for (int j = 0; j < 2; ++j) {
+            const int row = 16 * (2 * j + (tid >> 7)) + (tid & 15), q = 4 * ((tid >> 6) & 1) + ((tid >> 4) & 3);
+            *reinterpret_cast<u32x4*>(lds + S + S_C + (REV ? staged<128>(tid, j) : granule<128>(row, q))) = in.c[j];
+        }
         *reinterpret_cast<float*>(lds + S + S_G) = in.gl;      // the same value from every thread
     };
     // chunk i's set is i % 3; past the end the last chunk is fetched again and
@@ -678,9 +689,9 @@ __device__ __forceinline__ void spine_step(const Args& a, const Walk& k)
         sched_fence();
         read(1);
         const int c = REV ? k.nc - 1 - i : i;
-        byte* out = (REV ? a.dh : a.h) + ((size_t)(k.x0 + c) * a.Hv + k.vh) * kState + col * 256;
+        byte* out = (REV ? a.dh : a.h) + ((size_t)(k.x0 + c) * a.Hv + k.vh) * kState + 4096 * (4 * k.half + w) + 16 * lane;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) *reinterpret_cast<s16x8*>(out + 16 * (4 * ks + g)) = sb[ks];
+        for (int ks = 0; ks < 4; ++ks) *reinterpret_cast<s16x8*>(out + 1024 * ks) = sb[ks];
         sched_fence();
 #pragma unroll
         for (int t = 0; t < 8; ++t) st[t] *= gl;
@@ -831,7 +842,7 @@ gdn_bwd_grads_kernel(Args a)
         float hd = 0.f;                    // <h, dh'>
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int o = granule<256>(tid >> 4, tid & 15) + 8192 * i;
+            const int o = granule<256>(16 * (tid >> 8) + (tid & 15), (tid >> 4) & 15) + 8192 * i;
             *reinterpret_cast<u32x4*>(sH + o) = in.h[i];
             *reinterpret_cast<u32x4*>(sDH + o) = in.dh[i];
 #pragma unroll
