@@ -759,12 +759,15 @@ struct Small {
 constexpr int kGradLds = G_S + (int)sizeof(Small);
 static_assert(kGradLds <= 160 * 1024, "the grads kernel's LDS");
 
-template <typename TA>
+// SPLIT: a workgroup takes one v-head and leaves its part of dq and dk, in fp32,
+// where the v-head's h and dh' were, which only it reads.
+template <typename TA, bool SPLIT>
 __global__ void __launch_bounds__(kGradThreads)
 gdn_bwd_grads_kernel(Args a)
 {
     ChunkAt at;
-    const int x = blockIdx.x, kh = blockIdx.y, rep = a.Hv / a.Hk;
+    const int x = blockIdx.x, rep = a.Hv / a.Hk, kh = SPLIT ? blockIdx.y / rep : blockIdx.y;
+    const int vh0 = SPLIT ? blockIdx.y : kh * rep, vh1 = SPLIT ? vh0 + 1 : vh0 + rep;
     if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
     int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -833,7 +836,7 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
         for (int j = 0; j < 2; ++j) dq[i][j] = dk[i][j] = zero4();
 
-    for (int vh = kh * rep; vh < (kh + 1) * rep; ++vh) {
+    for (int vh = vh0; vh < vh1; ++vh) {
         L.fresh();
         asm volatile("" : "+v"(tid));      // likewise for all that is formed from it
         const int lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -1227,15 +1230,49 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int r = 32 * wr + 16 * j + n;
-        if (r < at.rows)
+        if constexpr (SPLIT) {
+            const size_t o = ((size_t)x * a.Hv + vh0) * kState + 512 * r + 4 * (32 * wc + 8 * g);
 #pragma unroll
-            for (int p = 0; p < 1; ++p) {
-                const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 32 * wc + 8 * g;
-                *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[2 * p][j], dq[2 * p + 1][j]);
-                *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[2 * p][j], dk[2 * p + 1][j]);
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<f32x4*>(a.h + o + 16 * i) = dq[i][j];
+                *reinterpret_cast<f32x4*>(a.dh + o + 16 * i) = dk[i][j];
             }
+        } else if (r < at.rows) {
+            const int64_t o = ((at.row0 + r) * a.Hk + kh) * D + 32 * wc + 8 * g;
+            *reinterpret_cast<u32x4*>(a.dq + o) = pack8(dq[0][j], dq[1][j]);
+            *reinterpret_cast<u32x4*>(a.dk + o) = pack8(dk[0][j], dk[1][j]);
+        }
     }
 }
+
+// dq (z = 0, 1) and dk (2, 3) of a k-head's chunk, 32 rows a workgroup: the parts of
+// its v-heads, added in their order.
+__global__ void __launch_bounds__(256)
+gdn_bwd_sum_kernel(Args a)
+{
+    ChunkAt at;
+    const int x = blockIdx.x, kh = blockIdx.y, rep = a.Hv / a.Hk, q = threadIdx.x & 7;
+    if (!bwd::chunk_at(x, a.cu, a.base, a.B, a.T, a.nc_dense, &at)) return;
+    const int r = 32 * (blockIdx.z & 1) + (threadIdx.x >> 3);
+    if (r >= at.rows) return;
+    const byte* p = (blockIdx.z < 2 ? a.h : a.dh) + ((size_t)x * a.Hv + (size_t)kh * rep) * kState + 512 * r + 64 * q;
+    f32x4 t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = reinterpret_cast<const f32x4*>(p)[e];
+    for (int i = 1; i < rep; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] += reinterpret_cast<const f32x4*>(p + (size_t)i * kState)[e];
+    uint16_t* out = (blockIdx.z < 2 ? a.dq : a.dk) + ((at.row0 + r) * a.Hk + kh) * D + 16 * q;
+    reinterpret_cast<u32x4*>(out)[0] = pack8(t[0], t[1]);
+    reinterpret_cast<u32x4*>(out)[1] = pack8(t[2], t[3]);
+}
+
+// Whether the gradients' workgroups take one v-head each: where every v-head finds a
+// compute unit (256) of its own, a k-head's v-heads need not wait for each other
+// (8 chunks x 2 k-heads x 3 v-heads: 34 us whole, 15 + 4 with the sum). From there on
+// the parts cost more than the turns: 8 x 16 x 3 takes 40 us whole and 37 + 5 split,
+// 16 x 16 x 3 takes 50 and 61 + 9, 72 x 16 x 3 takes 239 and 270 + 42.
+bool split_heads(int64_t chunks, int Hk, int Hv) { return Hv > Hk && chunks * Hv <= 256; }
 
 struct Layout {
     size_t base, heads, h, dh, total;
@@ -1259,13 +1296,18 @@ hipError_t launch_typed(const Args& k, int64_t chunks, hipStream_t s)
     hipError_t e;
     if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_prep_kernel<TA>), kPrepLds)) != hipSuccess) return e;
     if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_spine_kernel<TA>), kSpineLds)) != hipSuccess) return e;
-    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_grads_kernel<TA>), kGradLds)) != hipSuccess) return e;
+    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_grads_kernel<TA, false>), kGradLds)) != hipSuccess) return e;
+    if ((e = allow_lds(reinterpret_cast<const void*>(gdn_bwd_grads_kernel<TA, true>), kGradLds)) != hipSuccess) return e;
     if (k.cu) hipLaunchKernelGGL(gdn_bwd_table_kernel, dim3(1), dim3(256), 0, s, k.cu, k.B, k.T, k.base);
     if (chunks > 0)
         hipLaunchKernelGGL((gdn_bwd_prep_kernel<TA>), dim3((unsigned)chunks, k.Hv), dim3(256), kPrepLds, s, k);
     hipLaunchKernelGGL((gdn_bwd_spine_kernel<TA>), dim3(k.Hv * 2, k.B, 2), dim3(kSpineThreads), kSpineLds, s, k);
-    if (chunks > 0)
-        hipLaunchKernelGGL((gdn_bwd_grads_kernel<TA>), dim3((unsigned)chunks, k.Hk), dim3(kGradThreads), kGradLds, s, k);
+    if (chunks > 0 && split_heads(chunks, k.Hk, k.Hv)) {
+        hipLaunchKernelGGL((gdn_bwd_grads_kernel<TA, true>), dim3((unsigned)chunks, k.Hv), dim3(kGradThreads), kGradLds, s, k);
+        hipLaunchKernelGGL(gdn_bwd_sum_kernel, dim3((unsigned)chunks, k.Hk, 4), dim3(256), 0, s, k);
+    } else if (chunks > 0) {
+        hipLaunchKernelGGL((gdn_bwd_grads_kernel<TA, false>), dim3((unsigned)chunks, k.Hk), dim3(kGradThreads), kGradLds, s, k);
+    }
     return hipGetLastError();
 }
 

@@ -113,6 +113,31 @@ def test_mfma_short(T):
         assert rel_err(out[n], ref[n].numpy()) <= BF16_MAX, n
 
 
+def test_mfma_heads_together():
+    # 33 chunks x 8 v-heads: more v-heads than compute units, a workgroup takes a k-head whole
+    say("mfma, k-heads whole")
+    check(inputs(33, 9, 4, 8, 128, 128, torch.bfloat16, True, True, seed=77), mfma=True)
+
+
+def test_mfma_heads_together_and_apart():
+    # 5 x 3 chunks x 18 v-heads go by k-heads, one sequence's 3 x 18 by v-heads. What belongs
+    # to a v-head is the same to the bit; dq and dk add the same fp32 products in another order
+    # (3 x 64 x 128 terms at most, far below 2^-16 of the largest entry), so the roundings to
+    # bf16 land at most a step apart: 2^-7 of the value.
+    say("mfma, together and apart")
+    inp = inputs(5, 150, 6, 18, 128, 128, torch.bfloat16, True, True, seed=78)
+    a, _ = gpu(inp)
+    for b in range(5):
+        one = {n: t[b:b + 1] if torch.is_tensor(t) else t for n, t in inp.items()}
+        c, _ = gpu(one)
+        for n in a:
+            x, y = a[n][b].float(), c[n][0].float()
+            if n in ("dq", "dk"):
+                assert bool(((x - y).abs() <= 2.0 ** -7 * x.abs() + 2.0 ** -16 * x.abs().max()).all()), (n, b)
+            else:
+                assert torch.equal(x, y), (n, b)
+
+
 LENS = [64, 0, 1, 130, 63, 0, 40]
 
 
