@@ -878,25 +878,20 @@ gdn_bwd_grads_kernel(Args a)
         lds_barrier();
 
         // columns 16 w .. + 15 of dv: x, u, ddelta, dx, rows under sig
-        f32x4 u[1][4], dx[1][4];
+        f32x4 u[4], dx[4];
         {
-            f32x4 kh4[1][4], kd[1][4];
+            f32x4 kh4[4], kd[4];
 #pragma unroll
-            for (int c = 0; c < 1; ++c)
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt) kh4[c][rt] = kd[c][rt] = zero4();
-            s16x8 hb[2][1], db[2][1], kf[2][4];    // by turns of the k-steps
+            for (int rt = 0; rt < 4; ++rt) kh4[rt] = kd[rt] = zero4();
+            s16x8 hb[2], db[2], kf[2][4];    // by turns of the k-steps
             auto read = [&](int ks) {
-#pragma unroll
-                for (int c = 0; c < 1; ++c) {
-                    hb[ks & 1][c] = row8<256>(L, G_H, w + c, ks);
-                    db[ks & 1][c] = row8<256>(L, G_DH, w + c, ks);
-                }
+                hb[ks & 1] = row8<256>(L, G_H, w, ks);
+                db[ks & 1] = row8<256>(L, G_DH, w, ks);
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt) kf[ks & 1][rt] = row8_sig<256>(L, G_K, rt, ks);
             };
-            s16x8 tf[4][2], pf[4][2], ob[1][2];
-            s16x4 vf[1][4];
+            s16x8 tf[4][2], pf[4][2], ob[2];
+            s16x4 vf[4];
             read(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -904,9 +899,7 @@ gdn_bwd_grads_kernel(Args a)
                     read(ks + 1);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 1; ++c)
-#pragma unroll
-                        for (int rt = 0; rt < 4; ++rt) vf[c][rt] = col4<256>(L, G_U, rt >> 1, rt & 1, w + c);
+                    for (int rt = 0; rt < 4; ++rt) vf[rt] = col4<256>(L, G_U, rt >> 1, rt & 1, w);
 #pragma unroll
                     for (int rt = 0; rt < 4; ++rt) {
                         tf[rt][0] = down_sig<128>(L, G_X, 0, rt);            // T lower triangular
@@ -915,40 +908,33 @@ gdn_bwd_grads_kernel(Args a)
                 }
                 sched_fence();
 #pragma unroll
-                for (int c = 0; c < 1; ++c)
-#pragma unroll
-                    for (int rt = 0; rt < 4; ++rt) {
-                        kh4[c][rt] = mfma(kf[ks & 1][rt], hb[ks & 1][c], kh4[c][rt]);
-                        kd[c][rt] = mfma(kf[ks & 1][rt], db[ks & 1][c], kd[c][rt]);
-                    }
+                for (int rt = 0; rt < 4; ++rt) {
+                    kh4[rt] = mfma(kf[ks & 1][rt], hb[ks & 1], kh4[rt]);
+                    kd[rt] = mfma(kf[ks & 1][rt], db[ks & 1], kd[rt]);
+                }
             }
 #pragma unroll
-            for (int c = 0; c < 1; ++c)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) ob[c][j] = down<256>(L, G_DO, j, w + c);
+            for (int j = 0; j < 2; ++j) ob[j] = down<256>(L, G_DO, j, w);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {                                 // P^T upper triangular
                 pf[rt][1] = row8_sig<128>(L, G_X + kSquare, rt, 1);
                 if (rt < 2) pf[rt][0] = row8_sig<128>(L, G_X + kSquare, rt, 0);
             }
             sched_fence();
-            f32x4 dd[1][4];
+            f32x4 dd[4];
+            f32x4 xv[4];
 #pragma unroll
-            for (int c = 0; c < 1; ++c) {
-                f32x4 xv[4];
+            for (int rt = 0; rt < 4; ++rt) {
+                kh4[rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
+                xv[rt] = widen(vf[rt]) - kh4[rt];
+            }
+            const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    kh4[c][rt] *= *reinterpret_cast<const f32x4*>(sm.ga + sig0(rt) + 8 * g);      // ga K h
-                    xv[rt] = widen(vf[c][rt]) - kh4[c][rt];
-                }
-                const s16x8 xb[2] = {frag(xv[0], xv[1]), frag(xv[2], xv[3])};
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    u[c][rt] = mfma(tf[rt][0], xb[0], zero4());
-                    if (rt >= 2) u[c][rt] = mfma(tf[rt][1], xb[1], u[c][rt]);
-                    dd[c][rt] = mfma(pf[rt][1], ob[c][1], zero4());
-                    if (rt < 2) dd[c][rt] = mfma(pf[rt][0], ob[c][0], dd[c][rt]);
-                }
+            for (int rt = 0; rt < 4; ++rt) {
+                u[rt] = mfma(tf[rt][0], xb[0], zero4());
+                if (rt >= 2) u[rt] = mfma(tf[rt][1], xb[1], u[rt]);
+                dd[rt] = mfma(pf[rt][1], ob[1], zero4());
+                if (rt < 2) dd[rt] = mfma(pf[rt][0], ob[0], dd[rt]);
             }
             // T^T's rows, in the place of P^T's
 #pragma unroll
@@ -961,34 +947,31 @@ gdn_bwd_grads_kernel(Args a)
             f32x4 rG[4], rB[4];
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) rG[rt] = rB[rt] = zero4();
+            f32x4 yv[4];
 #pragma unroll
-            for (int c = 0; c < 1; ++c) {
-                f32x4 yv[4];
+            for (int rt = 0; rt < 4; ++rt) {
+                const int r = sig0(rt) + 8 * g;
+                const f32x4 E = *reinterpret_cast<const f32x4*>(sm.E + r), bt = *reinterpret_cast<const f32x4*>(sm.beta + r);
+                const f32x4 ek = E * kd[rt];
+                dd[rt] += ek;
+                yv[rt] = bt * dd[rt];
+                rB[rt] += dd[rt] * u[rt];
+                const f32x4 Y = bt * u[rt] * ek;
+                rG[rt] -= Y;
+                sumY += (Y[0] + Y[1]) + (Y[2] + Y[3]);
+            }
+            const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    const int r = sig0(rt) + 8 * g;
-                    const f32x4 E = *reinterpret_cast<const f32x4*>(sm.E + r), bt = *reinterpret_cast<const f32x4*>(sm.beta + r);
-                    const f32x4 ek = E * kd[c][rt];
-                    dd[c][rt] += ek;
-                    yv[rt] = bt * dd[c][rt];
-                    rB[rt] += dd[c][rt] * u[c][rt];
-                    const f32x4 Y = bt * u[c][rt] * ek;
-                    rG[rt] -= Y;
-                    sumY += (Y[0] + Y[1]) + (Y[2] + Y[3]);
-                }
-                const s16x8 yb[2] = {frag(yv[0], yv[1]), frag(yv[2], yv[3])};
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    dx[c][rt] = mfma(pf[rt][1], yb[1], zero4());
-                    if (rt < 2) dx[c][rt] = mfma(pf[rt][0], yb[0], dx[c][rt]);
-                }
+            for (int rt = 0; rt < 4; ++rt) {
+                dx[rt] = mfma(pf[rt][1], yb[1], zero4());
+                if (rt < 2) dx[rt] = mfma(pf[rt][0], yb[0], dx[rt]);
             }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 f32x4 rg, rb;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    rg[s] = sum16(rG[rt][s] - dx[0][rt][s] * kh4[0][rt][s]);
+                    rg[s] = sum16(rG[rt][s] - dx[rt][s] * kh4[rt][s]);
                     rb[s] = sum16(rB[rt][s]);
                 }
                 if (n == 0) {
@@ -1002,15 +985,12 @@ gdn_bwd_grads_kernel(Args a)
         }
         lds_barrier();                     // V, T^T and P^T have been read
 #pragma unroll
-        for (int c = 0; c < 1; ++c)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int o = granule<128>(16 * w + n, 4 * j + g);
-                *reinterpret_cast<u32x4*>(sU + o) = pack8(u[c][2 * j], u[c][2 * j + 1]);
-                *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[c][2 * j], dx[c][2 * j + 1]);
-            }
+        for (int j = 0; j < 2; ++j) {
+            const int o = granule<128>(16 * w + n, 4 * j + g);
+            *reinterpret_cast<u32x4*>(sU + o) = pack8(u[2 * j], u[2 * j + 1]);
+            *reinterpret_cast<u32x4*>(sX + o) = pack8(dx[2 * j], dx[2 * j + 1]);
+        }
         lds_barrier();
-
 
         // u dh'^T, then do h^T and dx h^T; after them h and dh' are not needed any more
         const int rn[2] = {32 * wr + n, 32 * wr + 16 + n};
@@ -1076,15 +1056,12 @@ gdn_bwd_grads_kernel(Args a)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float s = 0.f;
+                const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, wc);
+                const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
 #pragma unroll
-                for (int p = 0; p < 1; ++p) {
-                    const s16x8 q8 = row8<256>(L, G_Q, 2 * wr + j, wc);
-                    const f32x4 q0 = widen_lo(q8), q1 = widen_hi(q8);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s = fmaf(t[2 * p][j][e], q0[e], s);
-                        s = fmaf(t[2 * p + 1][j][e], q1[e], s);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    s = fmaf(t[0][j][e], q0[e], s);
+                    s = fmaf(t[1][j][e], q1[e], s);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
