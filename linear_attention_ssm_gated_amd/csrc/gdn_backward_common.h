@@ -49,7 +49,6 @@ struct ChunkAt {
     int c;          // chunk within it
     int64_t row0;   // first row of the chunk
     int rows;       // rows of the chunk, 1..64
-    bool last;      // the sequence's last chunk
 };
 
 // Rows of sequence b: [row0, row0 + len); offsets outside [0, T] are clamped
@@ -67,30 +66,40 @@ __device__ __forceinline__ void seq_rows(const int32_t* cu, int b, int T, int64_
     }
 }
 
-// First chunk of each sequence, base[0 .. B] (one workgroup of 256 threads).
+// First chunk of each sequence, base[0 .. B] (one workgroup of 256 threads), at
+// most the T / C + B chunks that sequences one behind the other have: offsets out
+// of order can overlap, and their further chunks are left out (walk_chunks).
 __device__ __forceinline__ void chunk_table(const int32_t* cu, int B, int T, int32_t* base, int32_t* part)
 {
     const int tid = threadIdx.x;
     const int per = (B + 255) / 256;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int32_t s = 0;
+    const int64_t most = (int64_t)T / C + B;
+    int64_t s = 0;
     for (int b = b0; b < b1; ++b) {
         int64_t r0, len;
         seq_rows(cu, b, T, &r0, &len);
-        s += (int32_t)((len + C - 1) / C);
+        s = min(s + (len + C - 1) / C, most);
     }
-    part[tid] = s;
+    part[tid] = (int32_t)s;
     __syncthreads();
-    int32_t before = 0;
+    int64_t before = 0;
     for (int i = 0; i < tid; ++i) before += part[i];
-    if (tid == 255) base[B] = before + part[255];
-    s = before;
+    if (tid == 255) base[B] = (int32_t)min(before + part[255], most);
+    s = min(before, most);
     for (int b = b0; b < b1; ++b) {
-        base[b] = s;
+        base[b] = (int32_t)s;
         int64_t r0, len;
         seq_rows(cu, b, T, &r0, &len);
-        s += (int32_t)((len + C - 1) / C);
+        s = min(s + (len + C - 1) / C, most);
     }
+}
+
+// Chunks of sequence b, len rows, that have a place in the workspace.
+__device__ __forceinline__ int walk_chunks(const int32_t* cu, const int32_t* base, int b, int64_t len)
+{
+    const int n = (int)((len + C - 1) / C);
+    return cu ? min(n, base[b + 1] - base[b]) : n;
 }
 
 // Chunk x of the call; false beyond the last one (packed grids are sized for
@@ -118,7 +127,6 @@ __device__ __forceinline__ bool chunk_at(int x, const int32_t* cu, const int32_t
     at->c = c;
     at->row0 = row0 + (int64_t)c * C;
     at->rows = (int)min((int64_t)C, len - (int64_t)c * C);
-    at->last = (int64_t)(c + 1) * C >= len;
     return true;
 }
 

@@ -292,7 +292,7 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
 
     int64_t row0, len;
     bwd::seq_rows(a.cu, b, a.T, &row0, &len);
-    const int nc = (int)((len + C - 1) / C);
+    const int nc = bwd::walk_chunks(a.cu, a.ws.base, b, len);
     const int64_t x0 = a.cu ? a.ws.base[b] : (int64_t)b * a.nc_dense;
     const float* from = REV ? a.dht : a.h0;
     const size_t hoff = ((size_t)b * a.Hv + vh) * a.dk_ * a.dv_;

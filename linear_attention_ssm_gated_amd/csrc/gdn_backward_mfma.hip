@@ -545,7 +545,7 @@ struct Walk {
         kh = (int)(i / a.B);
         vh = kh * rep + g;
         bwd::seq_rows(a.cu, b, a.T, &row0, &len);
-        nc = (int)((len + C - 1) / C);
+        nc = bwd::walk_chunks(a.cu, a.base, b, len);
         x0 = a.cu ? a.base[b] : (int64_t)b * a.nc_dense;
     }
 };

@@ -182,6 +182,26 @@ def test_offsets_outside_the_rows_are_clamped():
         assert torch.equal(a[n], b[n]), n
 
 
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+def test_offsets_out_of_order_stay_in_the_workspace(io):
+    # twice 0 .. 640 in three sequences: 20 chunks where the workspace has 10 + 3
+    say("offsets out of order", io)
+    d = 128 if io == torch.bfloat16 else 32
+    inp = inputs(3, 0, 1, 2, d, d, io, True, True, lens=[640, 0, 0], seed=8)
+    inp["cu_seqlens"] = torch.tensor([0, 640, 0, 640], dtype=torch.int32)
+    g = to_dev(inp)
+    out = {n: torch.zeros(inp[n[1:]].shape, dtype=io, device=dev()) for n in NAMES}
+    code = gdn.GDN_BF16 if io == torch.bfloat16 else gdn.GDN_F32
+    n = gdn.gdn_backward_workspace_bytes(3, 640, 1, 2, d, d, code, code, packed=True)
+    ws = torch.full((n + (32 << 20),), 171, dtype=torch.uint8, device=dev())
+    dh0 = torch.zeros_like(g["h0"])
+    gdn.gdn_chunk_backward(g["q"], g["k"], g["v"], None, None, None, g["log_g"], g["beta"], g["h0"], g["dout"],
+                           g["dht"], out["dq"], out["dk"], out["dv"], out["dlog_g"], out["dbeta"], dh0, 3, 640, 1, 2,
+                           d, d, cu_seqlens=g["cu_seqlens"], workspace=ws[:n])
+    torch.cuda.synchronize()
+    assert bool((ws[n:] == 171).all())
+
+
 @pytest.mark.parametrize("lens", [None, [70, 1, 129]])
 def test_checkpoints_equal_their_values(lens):
     # a code times its power of two is a bf16 value: the MFMA route must give the
