@@ -39,29 +39,6 @@ template <int VEC> __device__ __forceinline__ void load_vec(const float* p, floa
         f[0] = *p;
     }
 }
-template <int VEC> __device__ __forceinline__ void load_vec(const uint16_t* p, float* f)
-{
-    if constexpr (VEC == 8) {
-        const u4 v = *reinterpret_cast<const u4*>(p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(v[j] << 16);
-            f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
-        }
-    } else {
-        f[0] = bf16_bits_to_f32(*p);
-    }
-}
-template <int VEC> __device__ __forceinline__ void load_vec(const uint8_t* p, float* f)
-{
-    if constexpr (VEC == 8) {
-        const u2 v = *reinterpret_cast<const u2*>(p);
-        ckpt_unpack4(v[0], f);
-        ckpt_unpack4(v[1], f + 4);
-    } else {
-        f[0] = ckpt_unpack1(*p);
-    }
-}
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));

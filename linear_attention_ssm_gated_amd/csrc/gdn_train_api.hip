@@ -11,7 +11,7 @@
 
 namespace gdn {
 hipError_t allow_lds(const void* kernel, size_t bytes)
-{
+try {
     static std::mutex mu;
     static std::set<std::pair<int, const void*>> allowed;
     int dev = -1;
@@ -22,6 +22,8 @@ hipError_t allow_lds(const void* kernel, size_t bytes)
     e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == hipSuccess) allowed.insert({dev, kernel});
     return e;
+} catch (...) {          // the set's memory: nothing leaves a C entry point
+    return hipErrorOutOfMemory;
 }
 }  // namespace gdn
 

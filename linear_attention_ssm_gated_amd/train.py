@@ -201,6 +201,17 @@ def gdn_chunk_backward(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, d
 
 # ---- allocation conveniences (torch allocates, the library computes) --------
 
+def _shaped(**want):
+    """Refuse a tensor whose shape the kernels would read beyond."""
+    for name, (t, shape) in want.items():
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _exps_shape(rows, d):
+    return rows, -(-d // CKPT8_GROUP)
+
+
 def _token_rows(t):
     """Token stride of a [T, H, d] tensor whose heads lie next to each other."""
     T, H, d = t.shape
@@ -217,7 +228,7 @@ def ckpt8_store(x, stream=None):
     d = x.shape[-1]
     rows = x.numel() // d if d else 0
     codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    exps = torch.empty((rows, -(-d // CKPT8_GROUP)), dtype=torch.uint8, device=x.device)
+    exps = torch.empty(_exps_shape(rows, d), dtype=torch.uint8, device=x.device)
     gdn_ckpt8_store(x, codes, exps, rows, d, d, stream=stream)
     return codes, exps
 
@@ -225,8 +236,10 @@ def ckpt8_store(x, stream=None):
 def ckpt8_load(codes, exps, dtype=torch.bfloat16, stream=None):
     """The values of an 8-bit checkpoint as a tensor of codes' shape."""
     d = codes.shape[-1]
+    rows = codes.numel() // d if d else 0
+    _shaped(exps=(exps, _exps_shape(rows, d)))
     y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    gdn_ckpt8_load(codes, exps, y, codes.numel() // d if d else 0, d, d, stream=stream)
+    gdn_ckpt8_load(codes, exps, y, rows, d, d, stream=stream)
     return y
 
 
@@ -234,14 +247,14 @@ def norm_forward(x, w, z=None, b=None, eps=1e-6, center=False, ckpt=False, strea
     """Norm of x [T, H, d], times silu(z).  Returns (y, checkpoints), the
     checkpoints a dict of x_codes, x_exps (and z_codes, z_exps) with ckpt=True."""
     T, H, d = x.shape
+    _shaped(z=(z, x.shape), w=(w, (d,)), b=(b, (d,)))
     y = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
     kept = {}
     if ckpt:
         for name, t in (("x", x), ("z", z)):
             if t is not None:
                 kept[name + "_codes"] = torch.empty((T, H, d), dtype=torch.float8_e4m3fn, device=x.device)
-                kept[name + "_exps"] = torch.empty((T * H, -(-d // CKPT8_GROUP)), dtype=torch.uint8,
-                                                   device=x.device)
+                kept[name + "_exps"] = torch.empty(_exps_shape(T * H, d), dtype=torch.uint8, device=x.device)
     gdn_norm_forward(x, z, w, b, y, kept.get("x_codes"), kept.get("x_exps"), kept.get("z_codes"),
                      kept.get("z_exps"), T, H, d, _token_rows(x), H * d if z is None else _token_rows(z),
                      H * d, eps, center, stream=stream)
@@ -252,6 +265,8 @@ def norm_backward(dy, x, w, z=None, b=None, x_exps=None, z_exps=None, eps=1e-6, 
     """Gradients of norm_forward from x and z, or from their code tensors with
     exps.  Returns a dict of dx, dw (and dz, db)."""
     T, H, d = x.shape
+    exps = _exps_shape(T * H, d)
+    _shaped(dy=(dy, x.shape), z=(z, x.shape), w=(w, (d,)), b=(b, (d,)), x_exps=(x_exps, exps), z_exps=(z_exps, exps))
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dy.device)  # noqa: E731
     g = dict(dx=new((T, H, d), dy.dtype), dw=new(d, torch.float32))
     if z is not None:
@@ -277,11 +292,17 @@ def chunk_backward(q, k, v, log_g, beta, dout, h0=None, dh_final=None, cu_seqlen
     else:
         B, T, Hk, dk = q.shape
     Hv, dv = v.shape[-2], v.shape[-1]
+    rows, state = q.shape[:-2], (B, Hv, dk, dv)
+    _shaped(k=(k, q.shape), v=(v, (*rows, Hv, dv)), log_g=(log_g, (*rows, Hv)), beta=(beta, (*rows, Hv)),
+            dout=(dout, v.shape), h0=(h0, state), dh_final=(dh_final, state))
+    n = rows.numel()
+    _shaped(q_exps=(q_exps, _exps_shape(n * Hk, dk)), k_exps=(k_exps, _exps_shape(n * Hk, dk)),
+            v_exps=(v_exps, _exps_shape(n * Hv, dv)))
     dt, dev = dout.dtype, dout.device
     new = lambda shape, t=dt: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
     g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dlog_g=new(log_g.shape), dbeta=new(beta.shape))
     if h0 is not None if want_dh0 is None else want_dh0:
-        g["dh0"] = new((B, Hv, dk, dv), torch.float32)
+        g["dh0"] = new(state, torch.float32)
     io = GDN_E4M3 if _is_codes(q) else _code(q)
     n = gdn_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, io, _code(dout), packed=cu_seqlens is not None)
     ws = new(n, torch.uint8) if n else None

@@ -190,3 +190,25 @@ def test_binding_refuses_cpu_tensors():
                                1, 4, 1, 1, 8, 8)
     with pytest.raises(TypeError):
         gdn.chunk_backward(q.half(), q.half(), q.half(), q[..., 0], q[..., 0], q.half())
+
+
+def test_conveniences_refuse_shapes_they_would_read_beyond():
+    q, v, g = torch.zeros(1, 5, 2, 8), torch.zeros(1, 5, 4, 8), torch.zeros(1, 5, 4)
+    good = dict(q=q, k=q, v=v, log_g=g, beta=g, dout=v)
+    bad = dict(k=q[:, :4], v=v[:, :4], log_g=g[:, :4], beta=g[..., :2], dout=v[..., :4], h0=torch.zeros(1, 2, 8, 8),
+               dh_final=torch.zeros(1, 4, 8, 4), q_exps=torch.zeros(5, 1, dtype=torch.uint8),
+               v_exps=torch.zeros(20, 2, dtype=torch.uint8))
+    for name, t in bad.items():
+        with pytest.raises(ValueError, match="must have shape"):
+            gdn.chunk_backward(**{**good, name: t})
+    x, w = torch.zeros(3, 2, 8), torch.zeros(8)
+    for kw in (dict(w=w[:4]), dict(w=w, z=x[:2]), dict(w=w, b=w[:1])):
+        with pytest.raises(ValueError, match="must have shape"):
+            gdn.norm_forward(x, **kw)
+    for kw in (dict(w=w[:4]), dict(w=w, z=x[:2]), dict(w=w, x_exps=torch.zeros(6, 2, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="must have shape"):
+            gdn.norm_backward(x, x, **kw)
+    with pytest.raises(ValueError, match="must have shape"):
+        gdn.norm_backward(x[:2], x, w)
+    with pytest.raises(ValueError, match="must have shape"):
+        gdn.ckpt8_load(torch.zeros(4, 130, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
