@@ -5,7 +5,14 @@
 //   spine   one workgroup per (sequence, v-head, 64 dv columns, direction):
 //           the states forwards and their gradients backwards in one launch
 //   grads   one workgroup per (chunk, k-head): the gradients of the chunk, the
-//           v-heads of the k-head in turn, dq and dk summed in registers
+//           v-heads of the k-head in turn, dq and dk summed in registers (short
+//           calls: one per v-head, and a sum over the k-head's)
+// 4576 tokens of 16 / 48 heads in bf16 take 466 us back to back (prep 95, spine
+// 164, grads 240), where the inputs and gradients alone would take 48 us at a large
+// copy's rate and the products 64 us at a large matrix product's; the generic route
+// takes 3.0 ms.  Matrices are rounded to bf16 where a product takes them (T, P, W,
+// U, Qt; h and dh' from their fp32 states; u, dx and the masked products), as the
+// matrix units need; sums, states, gates and statistics stay fp32.
 //
 // Operands.  v_mfma_f32_16x16x32_bf16: lane 16 g + n supplies A[n][8g .. 8g+7]
 // and B[8g .. 8g+7][n] of a 32-wide k-step and holds rows 4g .. 4g+3 of column
@@ -300,6 +307,10 @@ __device__ __forceinline__ float wave_scan(float x, int lane)
 extern __shared__ __attribute__((aligned(1024))) byte lds[];
 
 // ---- prep ------------------------------------------------------------------------
+// Four waves, two workgroups a compute unit.  T by 16 x 16 blocks in fp32; P diag(beta)
+// T, W, U and Qt are products with T's and (P beta T ga)'s columns as they lie
+// transposed in LDS.  Bound by the workspace it writes: 4576 tokens, 48 v-heads: 263
+// MB written and 103 MB read (counters) in 95 us, 3.9 TB/s.
 using bwd::kBP;                                // pitch of the fp32 matrix B
 constexpr int P_K = 0;                         // K
 constexpr int P_Q = P_K + kTile;               // Q, then V
@@ -508,8 +519,12 @@ gdn_bwd_prep_kernel(Args a)
 // two products follow each other in its registers.  Four load: the next chunks'
 // matrices through registers (three steps ahead) into the LDS stage that is not
 // being read, so that a load or an LDS write that waits for the compute unit's
-// memory path holds up no product (loads issued by the walking waves: 2.6 us a
-// step against the products' 0.3).
+// memory path holds up no product.  72 steps of 48 v-heads take 164 us (315 MB read
+// and 226 MB written by the counters, 3.3 TB/s), 197 us with four waves that did
+// both and without the XCD order of Walk.  A step's latency is the time: 4800 cycles
+// backwards, of which the products fill 770, the LDS reads about 2000 and the 72 KB
+// of matrices through the compute unit's memory path 2200.  Loading waves that also
+// wrote the states out (two barriers a step) took 172 us.
 // One stage of LDS holds a chunk's matrices: forwards W, K and U's columns,
 // backwards K, W, Qt and do's columns.
 constexpr int kCols = 64;
@@ -739,7 +754,15 @@ gdn_bwd_spine_kernel(Args a)
 
 // ---- grads -------------------------------------------------------------------------
 // Eight waves, two to a SIMD, so that one's products run under the other's vector
-// work and LDS reads.
+// work and LDS reads; the LDS holds a v-head whole (K, Q, do, V, h, dh', T, P), so one
+// workgroup a compute unit.  72 x 16 chunks and k-heads of three v-heads: 240 us (471
+// MB read, 100 MB written by the counters, 2.4 TB/s).  Nothing is full: LDS 35 % of
+// the cycles (a third more in bank conflicts), vector units 35 %, matrix units 14 %;
+// the time is the five barriers of a v-head, each behind a chain of reads, products
+// and rounding, and 4.5 rounds of workgroups, the last half empty.  Taken and dropped: four
+// waves with the next v-head in registers (250 us), eight with it (250 to 270 us, as
+// registers spill), h, dh', T and P by asynchronous loads to LDS under the last products
+// (234 to 239 us: the loads' time moves into the phases that they run under).
 constexpr int kGradThreads = 512;
 constexpr int G_K = 0;
 constexpr int G_Q = G_K + kTile;

@@ -11,7 +11,9 @@
 //
 // Both kernels are bound by HBM: store moves (element size + 1) bytes a value
 // in one pass, the group's maximum formed in registers across the 8 lanes
-// that hold it.
+// that hold it.  Measured, bf16 rows of 128: store 14.2 us for 4576 x 48 rows
+// (84.8 MB, 5.9 TB/s), load 9.7 us for 2371 x 48 (43.8 MB, 4.5 TB/s; a 1 GiB copy
+// reaches 5.15 TB/s on this card, and part of these sizes comes from the caches).
 #include "gdn_train_internal.h"
 
 namespace gdn {
@@ -172,7 +174,8 @@ size_t elem(int dtype) { return dtype == 0 ? 4 : 2; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The 16-wide kernels take rows of a multiple of 16 values that start on 16
-// bytes.  (4576 x 48 rows of 128 in bf16: 19 us against 60 us value by value.)
+// bytes (4576 x 48 rows of 128 in bf16: store 14.6 us against 38.1 us value by
+// value, load 15.8 us against 43.5 us).
 bool wide(const CkptArgs& a, const void* side, const void* codes)
 {
     return a.d % 16 == 0 && (a.stride * (int64_t)elem(a.dtype)) % 16 == 0 && aligned16(side) && aligned16(codes);
