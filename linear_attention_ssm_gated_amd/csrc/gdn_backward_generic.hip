@@ -533,15 +533,15 @@ gdn_backward_grads_kernel(Args a)
     // x = V - ga K h; ga K h and E K dh' stay in registers
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-            const int col = 16 * j + n;
+        const int col = 16 * j + n;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * w + 4 * g + s;
-                gkh[j][s] *= sg.ga[r];
-                ek[j][s] *= sg.E[r];
-                s1[r * vp + col] = gV[r * dvp + col] - gkh[j][s];
-            }
+        for (int s = 0; s < 4; ++s) {
+            const int r = 16 * w + 4 * g + s;
+            gkh[j][s] *= sg.ga[r];
+            ek[j][s] *= sg.E[r];
+            s1[r * vp + col] = gV[r * dvp + col] - gkh[j][s];
         }
+    }
     __syncthreads();
     // u = T x
     mm_tiles<C>(u, [&](int kb) { return tr[kb / 16]; }, [&](int j, int k) { return s1[k * vp + 16 * j + n]; });
@@ -551,29 +551,29 @@ gdn_backward_grads_kernel(Args a)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * w + 4 * g + s;
-                const float d = dd[j][s] + ek[j][s];
-                rY[s] = fmaf(sg.beta[r] * u[j][s], ek[j][s], rY[s]);
-                rB[s] = fmaf(d, u[j][s], rB[s]);
-                s1[r * vp + 16 * j + n] = u[j][s];
-                s3[r * vp + 16 * j + n] = sg.beta[r] * d;
-            }
+        for (int s = 0; s < 4; ++s) {
+            const int r = 16 * w + 4 * g + s;
+            const float d = dd[j][s] + ek[j][s];
+            rY[s] = fmaf(sg.beta[r] * u[j][s], ek[j][s], rY[s]);
+            rB[s] = fmaf(d, u[j][s], rB[s]);
+            s1[r * vp + 16 * j + n] = u[j][s];
+            s3[r * vp + 16 * j + n] = sg.beta[r] * d;
+        }
     __syncthreads();
     mm_tiles<C>(dx, [&](int kb) { return tc[kb / 16]; }, [&](int j, int k) { return s3[k * vp + 16 * j + n]; });
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-            const int col = 16 * j + n;
+        const int col = 16 * j + n;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * w + 4 * g + s;
-                s3[r * vp + col] = dx[j][s];
-                rG[s] = fmaf(-dx[j][s], gkh[j][s], rG[s]);
-                if (r < at.rows && col < a.dv_)
-                    Elem<TG>::store(static_cast<TG*>(a.dv) + ((at.row0 + r) * a.Hv + vh) * a.dv_ + col, dx[j][s]);
-            }
+        for (int s = 0; s < 4; ++s) {
+            const int r = 16 * w + 4 * g + s;
+            s3[r * vp + col] = dx[j][s];
+            rG[s] = fmaf(-dx[j][s], gkh[j][s], rG[s]);
+            if (r < at.rows && col < a.dv_)
+                Elem<TG>::store(static_cast<TG*>(a.dv) + ((at.row0 + r) * a.Hv + vh) * a.dv_ + col, dx[j][s]);
         }
+    }
     __syncthreads();
     // Zu = dx u^T and do u^T on and below the diagonal: X, N, dP o Gam
     f32x4 rX = {0, 0, 0, 0};
@@ -628,9 +628,9 @@ gdn_backward_grads_kernel(Args a)
         const int col = 16 * j + n;
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
-                c.h[t] = four(h + col * dvp + 16 * t + 4 * g);
-                c.dh[t] = four(dh + col * dvp + 16 * t + 4 * g);
-            }
+            c.h[t] = four(h + col * dvp + 16 * t + 4 * g);
+            c.dh[t] = four(dh + col * dvp + 16 * t + 4 * g);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int k = 16 * (e >> 2) + 4 * g + (e & 3);
@@ -648,15 +648,15 @@ gdn_backward_grads_kernel(Args a)
         f32x4 dq = {0, 0, 0, 0}, dk = {0, 0, 0, 0}, dxh = {0, 0, 0, 0}, udh = {0, 0, 0, 0}, doh = {0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < NV; ++t) {
-                const f32x4 o4 = four(s2 + ra * vp + 16 * t + 4 * g), x4 = four(s3 + ra * vp + 16 * t + 4 * g),
-                            u4 = four(s1 + ra * vp + 16 * t + 4 * g);
+            const f32x4 o4 = four(s2 + ra * vp + 16 * t + 4 * g), x4 = four(s3 + ra * vp + 16 * t + 4 * g),
+                        u4 = four(s1 + ra * vp + 16 * t + 4 * g);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    doh = mfma4(o4[s], now.h[t][s], doh);
-                    dxh = mfma4(x4[s], now.h[t][s], dxh);
-                    udh = mfma4(u4[s], now.dh[t][s], udh);
-                }
+            for (int s = 0; s < 4; ++s) {
+                doh = mfma4(o4[s], now.h[t][s], doh);
+                dxh = mfma4(x4[s], now.h[t][s], dxh);
+                udh = mfma4(u4[s], now.dh[t][s], udh);
             }
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int k = 16 * (e >> 2) + 4 * g + (e & 3);
