@@ -11,12 +11,14 @@
 // Products run on fp32 MFMA (16x16x4: exact fp32 operands); the chunk's running
 // sums of log_g and their differences are fp64, since a difference of two large
 // sums would lose the decay's digits.  Head sizes are padded with zeros to 32, 64
-// or 128 in the workspace, which the kernels know at compile time: with tile counts
-// of the call, every tile stood behind a branch of its own and its LDS reads were
-// waited for one by one (85 us for the gradients of 16 chunks x 6 heads of 64 x
-// 96, 58 now).  2 x 500 tokens of 2 / 6 heads, 64 x 96, with both end states take
-// 124 us back to back (prep 34, spine 31, grads 58, sum 5): 96 workgroups for 256
-// compute units, bound by the latency of their chains of fp32 products.
+// or 128, or 96 of dv, in the workspace, which the kernels know at compile time: with
+// tile counts of the call, every tile stood behind a branch of its own and its LDS
+// reads were waited for one by one (85 us for the gradients of 16 chunks x 6 heads
+// of 64 x 96; 58 with constants and 64 x 128, 51 with 64 x 96, 43 with eight waves for
+// four; 128 x 128 takes the same with either).  2 x 500 tokens of 2 / 6 heads, 64 x
+// 96, with both end states take 106 us back to back (prep 32, spine 31, grads 43, sum
+// 5): 96 workgroups for 256 compute units, bound by the latency of their chains of
+// fp32 products.
 #include "gdn_backward_common.h"
 
 #include <type_traits>
@@ -445,15 +447,19 @@ __device__ __forceinline__ float sum16(float x)
     return x;
 }
 
+// Eight waves: wave w of half p has rows 16 w .. + 15 of half the columns of dv, then
+// of Zu (p = 0) or do u^T (1), then of half the columns of dk.
+constexpr int kGradThreads = 512;
+
 template <int NK, int NV, typename TG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kGradThreads)
 gdn_backward_grads_kernel(Args a)
 {
     __shared__ Gates sg;
-    __shared__ float s_dG[C], s_db[C];        // row sums, later with the column sums
-    __shared__ float s_colX[4][C], s_colZ[4][C];
-    __shared__ float s_sum[4];
-    constexpr int dkp = 16 * NK, dvp = 16 * NV, vp = dvp + 4;
+    __shared__ float s_dG[2][C], s_db[2][C], s_Y[2][C];   // row sums of a half
+    __shared__ float s_colX[8][C], s_colZ[4][C];
+    __shared__ float s_sum[8];
+    constexpr int dkp = 16 * NK, dvp = 16 * NV, vp = dvp + 4, NH = NV / 2;
     float* s1 = lds_dyn;              // x, then u           [C][vp]
     float* s2 = s1 + C * vp;          // do
     float* s3 = s2 + C * vp;          // h, then dh' [dkp][vp], then beta ddelta, then dx
@@ -463,7 +469,8 @@ gdn_backward_grads_kernel(Args a)
     ChunkAt at;
     const int x = blockIdx.x, vh = blockIdx.y, rep = a.Hv / a.Hk, kh = vh / rep;
     if (!bwd::chunk_at(x, a.cu, a.ws.base, a.B, a.T, a.nc_dense, &at)) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, n = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, w = (tid >> 6) & 3, g = lane >> 4, n = lane & 15;
+    const int p = __builtin_amdgcn_readfirstlane(tid >> 8), cn = 16 * NH * p + n;   // this lane's first column of dv
     const float* gK = a.ws.groups + ((size_t)x * a.Hk + kh) * a.sz.group();
     const float* gQ = gK + C * dkp;
     const float* head = a.ws.heads + ((size_t)x * a.Hv + vh) * a.sz.head();
@@ -472,20 +479,11 @@ gdn_backward_grads_kernel(Args a)
     const float* dh = a.ws.dh + ((size_t)x * a.Hv + vh) * a.sz.state();
     const int ra = 16 * w + n;                // this lane's row as an A operand
 
-    // what does not wait for anything: this lane's rows of K and of T, and columns
-    // of T and P
-    f32x4 kr[NK], tr[4], tc[4], pc[4];
+    f32x4 kr[NK];                             // this lane's row of K
 #pragma unroll
     for (int t = 0; t < NK; ++t) kr[t] = four(gK + ra * dkp + 16 * t + 4 * g);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        tr[t] = four(gT + ra * C + 16 * t + 4 * g);
-        const float *p = gT + (16 * t + 4 * g) * C + ra, *q = gP + (16 * t + 4 * g) * C + ra;
-        tc[t] = f32x4{p[0], p[C], p[2 * C], p[3 * C]};
-        pc[t] = f32x4{q[0], q[C], q[2 * C], q[3 * C]};
-    }
     load_gates(a, at, vh, &sg);
-    for (int e = tid; e < C * dvp; e += kThreads) {
+    for (int e = tid; e < C * dvp; e += kGradThreads) {
         const int r = e / dvp, j = e % dvp;
         s2[r * vp + j] = r < at.rows && j < a.dv_
                              ? Elem<TG>::load(static_cast<const TG*>(a.dout) + ((at.row0 + r) * a.Hv + vh) * a.dv_ + j)
@@ -493,7 +491,7 @@ gdn_backward_grads_kernel(Args a)
     }
     // K h and K dh': the states through LDS
     f32x4 rG = {0, 0, 0, 0}, rB = {0, 0, 0, 0}, rY = {0, 0, 0, 0};
-    f32x4 gkh[NV], ek[NV], u[NV], dx[NV], dd[NV];
+    f32x4 gkh[NH], ek[NH], u[NH], dx[NH], dd[NH];
     clear(gkh);
     clear(ek);
     clear(u);
@@ -501,16 +499,19 @@ gdn_backward_grads_kernel(Args a)
     clear(dd);
     float part = 0.f;                         // <h, dh'>
     {
-        constexpr int per = dkp * dvp / 4 / kThreads;   // vectors of a state a thread holds
+        // vectors of a state a thread holds (32 x 32 and 32 x 96: the last one not in every thread)
+        constexpr int all = dkp * dvp / 4, per = (all + kGradThreads - 1) / kGradThreads;
+        auto held = [&](int i) { return all % kGradThreads == 0 || tid + kGradThreads * i < all; };
         f32x4 hv[per];
 #pragma unroll
-        for (int i = 0; i < per; ++i) hv[i] = four(h + 4 * (tid + kThreads * i));
+        for (int i = 0; i < per; ++i) hv[i] = held(i) ? four(h + 4 * (tid + kGradThreads * i)) : f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < per; ++i) {
-                const int e = 4 * (tid + kThreads * i);
+                const int e = 4 * (tid + kGradThreads * i);
+                if (!held(i)) break;
                 f32x4* at_e = reinterpret_cast<f32x4*>(s3 + (e / dvp) * vp + e % dvp);
                 if (half) {
                     const f32x4 o = *at_e;
@@ -521,19 +522,29 @@ gdn_backward_grads_kernel(Args a)
             }
             if (!half)
 #pragma unroll
-                for (int i = 0; i < per; ++i) hv[i] = four(dh + 4 * (tid + kThreads * i));
+                for (int i = 0; i < per; ++i)
+                    if (held(i)) hv[i] = four(dh + 4 * (tid + kGradThreads * i));
             __syncthreads();
             mm_tiles<dkp>(half ? ek : gkh, [&](int kb) { return kr[kb / 16]; },
-                          [&](int j, int k) { return s3[k * vp + 16 * j + n]; });
+                          [&](int j, int k) { return s3[k * vp + cn + 16 * j]; });
         }
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) part += __shfl_xor(part, o);
-    if (lane == 0) s_sum[w] = part;
+    if (lane == 0) s_sum[tid >> 6] = part;
+    // this lane's row of T, and columns of T and P
+    f32x4 tr[4], tc[4], pc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        tr[t] = four(gT + ra * C + 16 * t + 4 * g);
+        const float *ct = gT + (16 * t + 4 * g) * C + ra, *cp = gP + (16 * t + 4 * g) * C + ra;
+        tc[t] = f32x4{ct[0], ct[C], ct[2 * C], ct[3 * C]};
+        pc[t] = f32x4{cp[0], cp[C], cp[2 * C], cp[3 * C]};
+    }
     // x = V - ga K h; ga K h and E K dh' stay in registers
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int col = 16 * j + n;
+    for (int j = 0; j < NH; ++j) {
+        const int col = cn + 16 * j;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * w + 4 * g + s;
@@ -544,27 +555,27 @@ gdn_backward_grads_kernel(Args a)
     }
     __syncthreads();
     // u = T x
-    mm_tiles<C>(u, [&](int kb) { return tr[kb / 16]; }, [&](int j, int k) { return s1[k * vp + 16 * j + n]; });
+    mm_tiles<C>(u, [&](int kb) { return tr[kb / 16]; }, [&](int j, int k) { return s1[k * vp + cn + 16 * j]; });
     // ddelta = P^T do + E K dh'
-    mm_tiles<C>(dd, [&](int kb) { return pc[kb / 16]; }, [&](int j, int k) { return s2[k * vp + 16 * j + n]; });
+    mm_tiles<C>(dd, [&](int kb) { return pc[kb / 16]; }, [&](int j, int k) { return s2[k * vp + cn + 16 * j]; });
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NH; ++j)
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * w + 4 * g + s;
             const float d = dd[j][s] + ek[j][s];
             rY[s] = fmaf(sg.beta[r] * u[j][s], ek[j][s], rY[s]);
             rB[s] = fmaf(d, u[j][s], rB[s]);
-            s1[r * vp + 16 * j + n] = u[j][s];
-            s3[r * vp + 16 * j + n] = sg.beta[r] * d;
+            s1[r * vp + cn + 16 * j] = u[j][s];
+            s3[r * vp + cn + 16 * j] = sg.beta[r] * d;
         }
     __syncthreads();
-    mm_tiles<C>(dx, [&](int kb) { return tc[kb / 16]; }, [&](int j, int k) { return s3[k * vp + 16 * j + n]; });
+    mm_tiles<C>(dx, [&](int kb) { return tc[kb / 16]; }, [&](int j, int k) { return s3[k * vp + cn + 16 * j]; });
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int col = 16 * j + n;
+    for (int j = 0; j < NH; ++j) {
+        const int col = cn + 16 * j;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * w + 4 * g + s;
@@ -575,44 +586,37 @@ gdn_backward_grads_kernel(Args a)
         }
     }
     __syncthreads();
-    // Zu = dx u^T and do u^T on and below the diagonal: X, N, dP o Gam
-    f32x4 rX = {0, 0, 0, 0};
-    f32x4 zu[4], du[4];
-    clear(zu);
-    clear(du);
-    mm_tiles<dvp>(zu, [&](int kb) { return four(s3 + ra * vp + kb + 4 * g); },
-             [&](int j, int k) { return s1[(16 * j + n) * vp + k]; });
-    mm_tiles<dvp>(du, [&](int kb) { return four(s2 + ra * vp + kb + 4 * g); },
-             [&](int j, int k) { return s1[(16 * j + n) * vp + k]; });
+    // Zu = dx u^T or do u^T on and below the diagonal: X, N or dP o Gam
+    f32x4 rX = {0, 0, 0, 0}, z[4];
+    clear(z);
+    const float *sA = p ? s2 : s3, *gBP = p ? gP : gB;
+    float* sNM = p ? sM : sN;
+    mm_tiles<dvp>(z, [&](int kb) { return four(sA + ra * vp + kb + 4 * g); },
+                  [&](int j, int k) { return s1[(16 * j + n) * vp + k]; });
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float cx = 0.f, cz = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * w + 4 * g + s, c = 16 * j + n;
-            float nv = 0.f, mv = 0.f;
-            if (c <= r) {
-                const float e = decay(sg, r, c), bt = sg.beta[c];
-                mv = du[j][s] * bt;
+            float v = 0.f;
+            if (p ? c <= r : c < r) {
+                v = p ? z[j][s] * sg.beta[c] : -z[j][s] * sg.beta[c];
                 if (c < r) {
-                    const float bb = gB[r * C + c];
-                    nv = -zu[j][s] * bt;
-                    const float X = nv * bb + mv * gP[r * C + c];
+                    const float b = gBP[r * C + c], X = v * b;
                     rX[s] += X;
                     cx += X;
-                    cz = fmaf(bb, zu[j][s], cz);
-                    nv *= e;
+                    cz = fmaf(b, z[j][s], cz);
                 }
-                mv *= e;
+                v *= decay(sg, r, c);
             }
-            sN[r * kMP + c] = nv;
-            sM[r * kMP + c] = mv;
+            sNM[r * kMP + c] = v;
         }
         cx += __shfl_xor(cx, 16); cx += __shfl_xor(cx, 32);
         cz += __shfl_xor(cz, 16); cz += __shfl_xor(cz, 32);
         if (g == 0) {
-            s_colX[w][16 * j + n] = cx;
-            s_colZ[w][16 * j + n] = cz;
+            s_colX[4 * p + w][16 * j + n] = cx;
+            if (p == 0) s_colZ[w][16 * j + n] = cz;
         }
     }
     __syncthreads();
@@ -638,12 +642,13 @@ gdn_backward_grads_kernel(Args a)
             c.q[e] = gQ[k * dkp + col];
         }
     };
-    constexpr bool ahead = NV < 8;            // a wide tile's columns fill the registers once
-    if (ahead) fetch(now, 0);
-    for (int j = 0; j < NK; ++j) {
+    constexpr bool ahead = NV < 6;            // a wide tile's columns fill the registers once
+    const int j0 = NK / 2 * p;
+    if (ahead) fetch(now, j0);
+    for (int j = j0; j < j0 + NK / 2; ++j) {
         const int col = 16 * j + n;
         if (!ahead) fetch(now, j);
-        else fetch(next, min(j + 1, NK - 1));
+        else fetch(next, min(j + 1, j0 + NK / 2 - 1));
         __builtin_amdgcn_sched_barrier(0);
         f32x4 dq = {0, 0, 0, 0}, dk = {0, 0, 0, 0}, dxh = {0, 0, 0, 0}, udh = {0, 0, 0, 0}, doh = {0, 0, 0, 0};
 #pragma unroll
@@ -681,29 +686,32 @@ gdn_backward_grads_kernel(Args a)
         }
         if (ahead) now = next;
     }
-    __syncthreads();                          // E has been read by every wave
     // row sums over the columns' 16 lanes
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const float G = sum16(rG[s] + rX[s]), Bt = sum16(rB[s]), Y = sum16(rY[s]);
         const int r = 16 * w + 4 * g + s;
         if (n == 0) {
-            s_dG[r] = G - Y;
-            s_db[r] = Bt;
-            sg.E[r] = Y;                      // E is not used again
+            s_dG[p][r] = G - Y;
+            s_db[p][r] = Bt;
+            s_Y[p][r] = Y;
         }
     }
     __syncthreads();
     if (tid < C) {                            // one wave: column sums, the last row's terms, the running sum
         float cx = 0.f, cz = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { cx += s_colX[i][tid]; cz += s_colZ[i][tid]; }
-        double d = (double)s_dG[tid] - (double)cx;
-        double Y = sg.E[tid];
+        for (int i = 0; i < 8; ++i) cx += s_colX[i][tid];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cz += s_colZ[i][tid];
+        double d = (double)(s_dG[0][tid] + s_dG[1][tid]) - (double)cx;
+        double Y = s_Y[0][tid] + s_Y[1][tid];
 #pragma unroll
         for (int o = 32; o; o >>= 1) Y += __shfl_xor(Y, o);
         if (tid == C - 1) {
-            const double hd = (double)s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+            double hd = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hd += s_sum[i];
             d += Y + (double)sg.ga[C - 1] * hd;
         }
 #pragma unroll
@@ -714,7 +722,7 @@ gdn_backward_grads_kernel(Args a)
         if (tid < at.rows) {
             const int64_t r = (at.row0 + tid) * a.Hv + vh;
             Elem<TG>::store(static_cast<TG*>(a.dg) + r, (float)d);
-            Elem<TG>::store(static_cast<TG*>(a.db) + r, s_db[tid] - cz);
+            Elem<TG>::store(static_cast<TG*>(a.db) + r, s_db[0][tid] + s_db[1][tid] - cz);
         }
     }
 }
@@ -743,7 +751,7 @@ gdn_backward_sum_kernel(Args a)
 }
 
 int padded(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
-Sizes sizes(int dk, int dv) { return Sizes{padded(dk), padded(dv)}; }
+Sizes sizes(int dk, int dv) { return Sizes{padded(dk), dv > 64 && dv <= 96 ? 96 : padded(dv)}; }
 
 struct Layout {
     size_t base, heads, groups, h, dh, part, total;
@@ -775,30 +783,36 @@ size_t grads_lds(const Sizes& s)
 }
 int slices_of(const Sizes& s) { return (s.dvp + kCols - 1) / kCols; }
 
-// The head sizes' tile counts, 2, 4 or 8 each, as compile-time constants.
+// The head sizes' tile counts as compile-time constants: 2, 4 or 8 of dk, whose
+// state tiles the spine's four waves share out evenly, and also 6 of dv.
 template <typename F>
-hipError_t with_tiles(int n, F&& f)
+hipError_t with_dk(int n, F&& f)
 {
     if (n == 32) return f(std::integral_constant<int, 2>());
     if (n == 64) return f(std::integral_constant<int, 4>());
     return f(std::integral_constant<int, 8>());
 }
+template <typename F>
+hipError_t with_dv(int n, F&& f)
+{
+    return n == 96 ? f(std::integral_constant<int, 6>()) : with_dk(n, f);
+}
 
 template <typename K>
-hipError_t run(K kernel, dim3 grid, size_t lds, hipStream_t s, const Args& k)
+hipError_t run(K kernel, dim3 grid, unsigned threads, size_t lds, hipStream_t s, const Args& k)
 {
     const hipError_t e = lds > 0 ? allow_lds(reinterpret_cast<const void*>(kernel), lds) : hipSuccess;
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), lds, s, k);
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, s, k);
     return hipGetLastError();
 }
 
 template <typename TA>
 hipError_t launch_prep(const Args& k, unsigned chunks, hipStream_t s)
 {
-    return with_tiles(k.sz.dkp, [&](auto nk) {
-        return with_tiles(k.sz.dvp, [&](auto nv) {
-            return run(gdn_backward_prep_kernel<nk.value, nv.value, TA>, dim3(chunks, k.Hv), prep_lds(k.sz), s, k);
+    return with_dk(k.sz.dkp, [&](auto nk) {
+        return with_dv(k.sz.dvp, [&](auto nv) {
+            return run(gdn_backward_prep_kernel<nk.value, nv.value, TA>, dim3(chunks, k.Hv), kThreads, prep_lds(k.sz), s, k);
         });
     });
 }
@@ -807,19 +821,20 @@ template <typename TG>
 hipError_t launch_walk(const Args& k, unsigned chunks, hipStream_t s)
 {
     const int slices = slices_of(k.sz);
-    hipError_t e = with_tiles(k.sz.dkp, [&](auto nk) {
+    hipError_t e = with_dk(k.sz.dkp, [&](auto nk) {
         hipLaunchKernelGGL((gdn_backward_spine_kernel<nk.value, TG>), dim3(k.Hv * slices, k.B, 2), dim3(kThreads), 0,
                            s, k, slices);
         return hipGetLastError();
     });
     if (e != hipSuccess || chunks == 0) return e;
-    e = with_tiles(k.sz.dkp, [&](auto nk) {
-        return with_tiles(k.sz.dvp, [&](auto nv) {
-            return run(gdn_backward_grads_kernel<nk.value, nv.value, TG>, dim3(chunks, k.Hv), grads_lds(k.sz), s, k);
+    e = with_dk(k.sz.dkp, [&](auto nk) {
+        return with_dv(k.sz.dvp, [&](auto nv) {
+            return run(gdn_backward_grads_kernel<nk.value, nv.value, TG>, dim3(chunks, k.Hv), kGradThreads, grads_lds(k.sz), s,
+                       k);
         });
     });
     if (e != hipSuccess || k.Hv == k.Hk) return e;
-    return run(gdn_backward_sum_kernel<TG>, dim3(chunks, k.Hk, 8), 0, s, k);
+    return run(gdn_backward_sum_kernel<TG>, dim3(chunks, k.Hk, 8), kThreads, 0, s, k);
 }
 
 }  // namespace

@@ -84,6 +84,22 @@ def test_generic(case):
     check(inputs(B, T, Hk, Hv, dk, dv, torch.float32, h0, dht, seed=T), mfma=False)
 
 
+@pytest.mark.parametrize("dk", [20, 50, 100])
+@pytest.mark.parametrize("dv", [20, 50, 90, 120])
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+def test_generic_head_sizes(dk, dv, io):
+    # every pair of padded sizes, with the end state's and the start state's gradients;
+    # bf16 gradients of fp32 sums are one rounding off (2^-8 of the value)
+    say("generic sizes", dk, dv, io)
+    inp = inputs(1, 70, 1, 2, dk, dv, io, True, True, seed=dk + dv)
+    out, route = gpu(inp)
+    assert route.startswith("gdn_backward_prep"), route
+    ref = train_ref.delta_rule_grads(inp, inp["dout"], inp["dht"])
+    for n in out:
+        bound = F32_MAX + (2.0 ** -8 if out[n].dtype == torch.bfloat16 else 0.0)
+        assert rel_err(out[n], ref[n].numpy()) <= bound, (n, rel_err(out[n], ref[n].numpy()))
+
+
 MFMA = [
     # B, T, Hk, Hv, h0, dht
     (1, 16, 1, 1, False, False),
