@@ -2,7 +2,7 @@
 // or 8-bit inputs, any dk, dv <= 128.  The formulas are in
 // gdn_backward_common.h.  Three kernels:
 //   prep    one workgroup per (chunk, v-head): B, P, T, W, U, Qt
-//   spine   one workgroup per (sequence, v-head, 32 dv columns, direction): the
+//   spine   one workgroup per (sequence, v-head, 16 or 32 dv columns, direction): the
 //           states walked forwards and their gradients backwards, both in the
 //           same launch, every chunk's start state and end gradient written
 //   grads   one workgroup per (chunk, v-head): the chunk's gradients; dq and dk
@@ -16,7 +16,7 @@
 // reads were waited for one by one (85 us for the gradients of 16 chunks x 6 heads
 // of 64 x 96; 58 with constants and 64 x 128, 51 with 64 x 96, 43 with eight waves for
 // four; 128 x 128 takes the same with either).  2 x 500 tokens of 2 / 6 heads, 64 x
-// 96, with both end states take 106 us back to back (prep 32, spine 31, grads 43, sum
+// 96, with both end states take 98 us back to back (prep 32, spine 22, grads 42, sum
 // 5): 96 workgroups for 256 compute units, bound by the latency of their chains of
 // fp32 products.
 #include "gdn_backward_common.h"
@@ -31,8 +31,6 @@ using bwd::ChunkAt;
 
 constexpr int kThreads = 256;
 constexpr int kMP = bwd::kBP;        // pitch of a 64 x 64 matrix in LDS
-constexpr int kCols = 32;           // dv columns of a spine workgroup
-constexpr int kSP = kCols + 4;
 
 using bwd::f32x4;
 using bwd::mfma4;
@@ -283,11 +281,11 @@ gdn_backward_prep_kernel(Args a)
 // A step's operands come from memory as they are, fetched while the step before
 // runs (two register sets): wave w needs rows 16 w .. + 15 of the left matrix (W,
 // or K) and columns of state tiles w and w + 4 of the right ones (K, or W and Qt).
-template <int NK, typename TG, bool REV>
-__device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS)[16 * NK][kSP],
-                                           float (&sD)[C][kSP], float (&sO)[C][kSP])
+template <int NK, int NC, typename TG, bool REV>
+__device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS)[16 * NK][16 * NC + 4],
+                                           float (&sD)[C][16 * NC + 4], float (&sO)[C][16 * NC + 4])
 {
-    constexpr int dkp = 16 * NK, NI = NK > 4 ? 2 : 1;   // state tiles a wave holds
+    constexpr int dkp = 16 * NK, NI = NK > 4 ? 2 : 1, kCols = 16 * NC;   // NI: row tiles of the state that a wave holds
     const int dvp = a.sz.dvp;
     const int vh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * kCols, b = blockIdx.y;
     const int kh = vh / (a.Hv / a.Hk);
@@ -301,12 +299,12 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
     const float* from = REV ? a.dht : a.h0;
     const size_t hoff = ((size_t)b * a.Hv + vh) * a.dk_ * a.dv_;
 
-    // wave w holds state rows of tiles w and w + 4, both column tiles
-    f32x4 st[NI][2];
+    // wave w holds state rows of tiles w and w + 4, every column tile
+    f32x4 st[NI][NC];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int r = 16 * (w + 4 * i) + 4 * g + s, c = col0 + 16 * j + n;
@@ -316,7 +314,7 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
     struct Regs {
         f32x4 left[NK];      // row 16 w + n, k = 16 t + 4 g .. + 3
         float right[NI][16], qt[NI][16];   // column 16 (w + 4 i) + n, rows 16 (e / 4) + 4 g + e % 4
-        float add[2][4];            // U (rows 16 w + 4 g + s), or do (this thread's eight)
+        float add[NC][4];           // U (rows 16 w + 4 g + s), or do (this thread's 4 NC)
         double gl;
     } in0, in1;
     auto chunk_of = [&](int i) { return (size_t)(x0 + (REV ? nc - 1 - i : i)); };
@@ -340,7 +338,7 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
         if constexpr (REV) {
             const int64_t first = row0 + (int64_t)(nc - 1 - i) * C;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4 * NC; ++e) {
                 const int r = (tid + kThreads * e) / kCols, j = (tid + kThreads * e) % kCols;
                 in.add[e >> 2][e & 3] = first + r < row0 + len && col0 + j < a.dv_
                                             ? Elem<TG>::load(static_cast<const TG*>(a.dout) + ((first + r) * a.Hv + vh) * a.dv_ + col0 + j)
@@ -348,7 +346,7 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NC; ++j)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) in.add[j][s] = gU[(16 * w + 4 * g + s) * dvp + col0 + 16 * j + n];
         }
@@ -362,7 +360,7 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
 #pragma unroll
         for (int i2 = 0; i2 < NI; ++i2)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NC; ++j)
                 if (some)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
@@ -372,19 +370,19 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
                     }
         if constexpr (REV)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sO[(tid + kThreads * e) / kCols][(tid + kThreads * e) % kCols] = in.add[e >> 2][e & 3];
+            for (int e = 0; e < 4 * NC; ++e) sO[(tid + kThreads * e) / kCols][(tid + kThreads * e) % kCols] = in.add[e >> 2][e & 3];
         bwd::lds_barrier();
         // rows 16 w .. + 15 of W h (of K dh')
-        f32x4 d[2];
+        f32x4 d[NC];
         clear(d);
 #pragma unroll
         for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) d[j] = mfma4(in.left[kt][s], sS[16 * kt + 4 * g + s][16 * j + n], d[j]);
+                for (int j = 0; j < NC; ++j) d[j] = mfma4(in.left[kt][s], sS[16 * kt + 4 * g + s][16 * j + n], d[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int s = 0; s < 4; ++s) sD[16 * w + 4 * g + s][16 * j + n] = REV ? -d[j][s] : in.add[j][s] - d[j][s];
         bwd::lds_barrier();
@@ -393,12 +391,12 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
 #pragma unroll
             for (int i2 = 0; i2 < NI; ++i2)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) st[i2][j] *= gL;
+                for (int j = 0; j < NC; ++j) st[i2][j] *= gL;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int k = 16 * (e >> 2) + 4 * g + (e & 3);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NC; ++j) {
                     const float dv = sD[k][16 * j + n], ov = REV ? sO[k][16 * j + n] : 0.f;
 #pragma unroll
                     for (int i2 = 0; i2 < NI; ++i2) {
@@ -417,9 +415,9 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
     }
     if (REV && a.dh0)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NC; ++j)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int r = 16 * (w + 4 * i) + 4 * g + s, c = col0 + 16 * j + n;
@@ -427,15 +425,15 @@ __device__ __forceinline__ void spine_walk(const Args& a, int slices, float (&sS
                 }
 }
 
-template <int NK, typename TG>
+template <int NK, int NC, typename TG>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_backward_spine_kernel(Args a, int slices)
 {
-    __shared__ float sS[16 * NK][kSP];   // the state's columns
-    __shared__ float sD[C][kSP];                // U - W h, or -K dh'
-    __shared__ float sO[C][kSP];                // do
-    if (blockIdx.z == 0) spine_walk<NK, TG, false>(a, slices, sS, sD, sO);
-    else spine_walk<NK, TG, true>(a, slices, sS, sD, sO);
+    __shared__ float sS[16 * NK][16 * NC + 4];   // the state's columns
+    __shared__ float sD[C][16 * NC + 4];         // U - W h, or -K dh'
+    __shared__ float sO[C][16 * NC + 4];         // do
+    if (blockIdx.z == 0) spine_walk<NK, NC, TG, false>(a, slices, sS, sD, sO);
+    else spine_walk<NK, NC, TG, true>(a, slices, sS, sD, sO);
 }
 
 // ---- grads -----------------------------------------------------------------------
@@ -781,7 +779,10 @@ size_t grads_lds(const Sizes& s)
     const size_t row = s.dvp + 4, tail = C * row + 2 * (size_t)C * kMP, state = s.dkp * row;
     return (2 * C * row + (tail > state ? tail : state)) * sizeof(float);
 }
-int slices_of(const Sizes& s) { return (s.dvp + kCols - 1) / kCols; }
+// 16-column tiles of dv that a spine workgroup walks: two, or one where twice the
+// workgroups still find a compute unit each (2 x 500 tokens of 6 heads, 64 x 96:
+// 31 us with two, 22 with one).  Either gives the same bits.
+int spine_tiles(const Sizes& s, int Hv, int B) { return (int64_t)Hv * (s.dvp / 32) * B * 2 <= 128 ? 1 : 2; }
 
 // The head sizes' tile counts as compile-time constants: 2, 4 or 8 of dk, whose
 // state tiles the spine's four waves share out evenly, and also 6 of dv.
@@ -820,10 +821,13 @@ hipError_t launch_prep(const Args& k, unsigned chunks, hipStream_t s)
 template <typename TG>
 hipError_t launch_walk(const Args& k, unsigned chunks, hipStream_t s)
 {
-    const int slices = slices_of(k.sz);
+    const int tiles = spine_tiles(k.sz, k.Hv, k.B), slices = k.sz.dvp / (16 * tiles);
     hipError_t e = with_dk(k.sz.dkp, [&](auto nk) {
-        hipLaunchKernelGGL((gdn_backward_spine_kernel<nk.value, TG>), dim3(k.Hv * slices, k.B, 2), dim3(kThreads), 0,
-                           s, k, slices);
+        const dim3 grid(k.Hv * slices, k.B, 2);
+        if (tiles == 1)
+            hipLaunchKernelGGL((gdn_backward_spine_kernel<nk.value, 1, TG>), grid, dim3(kThreads), 0, s, k, slices);
+        else
+            hipLaunchKernelGGL((gdn_backward_spine_kernel<nk.value, 2, TG>), grid, dim3(kThreads), 0, s, k, slices);
         return hipGetLastError();
     });
     if (e != hipSuccess || chunks == 0) return e;
@@ -852,7 +856,7 @@ Geometry backward_generic_geometry(const BackwardArgs& a)
 {
     const Sizes sz = sizes(a.dk, a.dv);
     return Geometry{"gdn_backward_prep_kernel+gdn_backward_spine_kernel+gdn_backward_grads_kernel",
-                    {(unsigned)(a.Hv * slices_of(sz)), (unsigned)a.B, 2}, kThreads, (unsigned)grads_lds(sz)};
+                    {(unsigned)(a.Hv * (sz.dvp / (16 * spine_tiles(sz, a.Hv, a.B)))), (unsigned)a.B, 2}, kThreads, (unsigned)grads_lds(sz)};
 }
 
 hipError_t launch_backward_generic(const BackwardArgs& a, hipStream_t s)

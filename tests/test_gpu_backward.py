@@ -100,6 +100,19 @@ def test_generic_head_sizes(dk, dv, io):
         assert rel_err(out[n], ref[n].numpy()) <= bound, (n, rel_err(out[n], ref[n].numpy()))
 
 
+def test_generic_wide_and_narrow_walks():
+    # 9 sequences of 8 v-heads, 64 columns: walks of 32 columns; one sequence: of 16.
+    # A column's products are the same ones in the same order.
+    say("generic walks")
+    inp = inputs(9, 70, 4, 8, 40, 50, torch.float32, True, True, seed=12)
+    a, _ = check(inp, mfma=False)
+    for b in range(9):
+        one = {n: t[b:b + 1] if torch.is_tensor(t) else t for n, t in inp.items()}
+        c, _ = gpu(one)
+        for n in a:
+            assert torch.equal(a[n][b], c[n][0]), (n, b)
+
+
 MFMA = [
     # B, T, Hk, Hv, h0, dht
     (1, 16, 1, 1, False, False),
