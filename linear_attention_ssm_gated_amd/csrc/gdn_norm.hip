@@ -196,7 +196,11 @@ struct Place {
             ++t;
         }
     }
-    __device__ __forceinline__ int64_t at(int64_t stride, const Shape& s) const { return (int64_t)t * stride + h * s.d; }
+    // (the heads of one token alone may hold more than 2^31 values)
+    __device__ __forceinline__ int64_t at(int64_t stride, const Shape& s) const
+    {
+        return (int64_t)t * stride + (int64_t)h * s.d;
+    }
 };
 
 // The row's values minus their mean (center), and 1 / sqrt(var + eps).  The

@@ -188,3 +188,22 @@ def test_gradient_against_differences():
         got = float((g["d" + n].cpu().double() * step).sum())
         # differences are off by h^2 times a third derivative of order 1 per value
         assert abs(got - want) <= 1e-4 * max(1.0, abs(want)), n
+
+
+def test_heads_of_one_token_past_32_bits():
+    # one token of 2^18 + 3 heads of 8192: a head's offset passes 2^31 values.  The
+    # same rows as tokens of one head are the same bits
+    say("norm, one token's heads past 2^31 values")
+    H, d = (1 << 18) + 3, 8192
+    gen = torch.Generator(dev()).manual_seed(5)
+    x, dy = (torch.randn(1, H, d, generator=gen, device=dev(), dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand(d, generator=gen, device=dev()) + 0.5
+    one, _ = gdn.norm_forward(x, w, z=dy)
+    rows, _ = gdn.norm_forward(x.view(H, 1, d), w, z=dy.view(H, 1, d))
+    assert torch.equal(one.view(H, 1, d), rows)
+    close(rows[-3:], train_ref.norm(x[0, -3:, None].cpu().double(), w.cpu().double(), dy[0, -3:, None].cpu().double()), "y")
+    del one, rows
+    one = gdn.norm_backward(dy, x, w, z=x)
+    rows = gdn.norm_backward(dy.view(H, 1, d), x.view(H, 1, d), w, z=x.view(H, 1, d))
+    for n in one:
+        assert torch.equal(one[n].flatten(), rows[n].flatten()), n
