@@ -8,6 +8,7 @@ library is not built, or a call is refused, an exception says so.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -119,6 +120,23 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, device):
+    """Context of a convenience's allocations and launch.  Workspace and outputs
+    come from the memory pool of the stream that uses them: memory dropped on
+    return is then handed out again behind the launched work only, and taken
+    behind what used it before."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream and the tensors of a call must be on one GPU")
+    return torch.cuda.stream(stream)
+
+
 # ---- entry points, same names as the C ABI --------------------------------
 
 def gdn_prefill_workspace_bytes(B, T, Hk, Hv, dk, dv, chunk, io_dtype, packed=False) -> int:
@@ -213,6 +231,9 @@ def gdn_fold(h_table, stash, na_tab, hi_tables, slab_entries, engaged_flag, k_ro
 
 
 # ---- allocation conveniences (torch allocates, the library computes) ------
+# With stream= a convenience behaves like a torch operator under
+# torch.cuda.stream(stream): its outputs belong to that stream, and another
+# stream waits before it reads them.
 
 def gdn_ba_gates_workspace_bytes(m, n, k) -> int:
     return library().gdn_ba_gates_workspace_bytes(m, n, k)
@@ -239,11 +260,12 @@ def ba_gates(x, w, a_log, dt_bias, nv, vheads_per_group, gate_stride=None, strea
     m, k_stride = x.shape
     n, k = w.shape
     gs = 2 * nv if gate_stride is None else gate_stride
-    out = torch.empty((m, gs), dtype=torch.float32, device=x.device)
-    ws_n = gdn_ba_gates_workspace_bytes(m, n, k)
-    ws = torch.empty(ws_n, dtype=torch.uint8, device=x.device) if ws_n else None
-    route = gdn_ba_gates(x, w, a_log, dt_bias, out, m, n, k, k_stride, gs, nv, vheads_per_group,
-                         workspace=ws, stream=stream)
+    with _on_stream(stream, x.device):
+        out = torch.empty((m, gs), dtype=torch.float32, device=x.device)
+        ws_n = gdn_ba_gates_workspace_bytes(m, n, k)
+        ws = torch.empty(ws_n, dtype=torch.uint8, device=x.device) if ws_n else None
+        route = gdn_ba_gates(x, w, a_log, dt_bias, out, m, n, k, k_stride, gs, nv, vheads_per_group,
+                             workspace=ws, stream=stream)
     return out, route
 
 
@@ -262,14 +284,15 @@ def chunk_prefill(q, k, v, log_g, beta, h0=None, cu_seqlens=None, chunk=64, out_
     else:
         B, T, Hk, dk = q.shape
     Hv, dv = v.shape[-2], v.shape[-1]
-    out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
-    hf = torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=v.device) if want_state else None
-    ws_n = gdn_prefill_workspace_bytes(B, T, Hk, Hv, dk, dv, chunk, _dtype_code(q),
-                                       packed=cu_seqlens is not None)
-    ws = torch.empty(ws_n, dtype=torch.uint8, device=v.device) if ws_n else None
-    call = gdn_chunk_prefill_segmented if segmented else gdn_chunk_prefill
-    route = call(q, k, v, log_g, beta, h0, out, hf, B, T, Hk, Hv, dk, dv, chunk,
-                 cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
+    with _on_stream(stream, v.device):
+        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+        hf = torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=v.device) if want_state else None
+        ws_n = gdn_prefill_workspace_bytes(B, T, Hk, Hv, dk, dv, chunk, _dtype_code(q),
+                                           packed=cu_seqlens is not None)
+        ws = torch.empty(ws_n, dtype=torch.uint8, device=v.device) if ws_n else None
+        call = gdn_chunk_prefill_segmented if segmented else gdn_chunk_prefill
+        route = call(q, k, v, log_g, beta, h0, out, hf, B, T, Hk, Hv, dk, dv, chunk,
+                     cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
     return out, hf, route
 
 

@@ -200,6 +200,8 @@ def gdn_chunk_backward(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, d
 
 
 # ---- allocation conveniences (torch allocates, the library computes) --------
+# With stream= they behave like torch operators under torch.cuda.stream(stream):
+# workspace and outputs come from that stream's memory pool.
 
 def _shaped(**want):
     """Refuse a tensor whose shape the kernels would read beyond."""
@@ -227,9 +229,10 @@ def ckpt8_store(x, stream=None):
         raise ValueError("tensors must be contiguous")
     d = x.shape[-1]
     rows = x.numel() // d if d else 0
-    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    exps = torch.empty(_exps_shape(rows, d), dtype=torch.uint8, device=x.device)
-    gdn_ckpt8_store(x, codes, exps, rows, d, d, stream=stream)
+    with _gdn._on_stream(stream, x.device):
+        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        exps = torch.empty(_exps_shape(rows, d), dtype=torch.uint8, device=x.device)
+        gdn_ckpt8_store(x, codes, exps, rows, d, d, stream=stream)
     return codes, exps
 
 
@@ -238,8 +241,9 @@ def ckpt8_load(codes, exps, dtype=torch.bfloat16, stream=None):
     d = codes.shape[-1]
     rows = codes.numel() // d if d else 0
     _shaped(exps=(exps, _exps_shape(rows, d)))
-    y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    gdn_ckpt8_load(codes, exps, y, rows, d, d, stream=stream)
+    with _gdn._on_stream(stream, codes.device):
+        y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        gdn_ckpt8_load(codes, exps, y, rows, d, d, stream=stream)
     return y
 
 
@@ -248,16 +252,17 @@ def norm_forward(x, w, z=None, b=None, eps=1e-6, center=False, ckpt=False, strea
     checkpoints a dict of x_codes, x_exps (and z_codes, z_exps) with ckpt=True."""
     T, H, d = x.shape
     _shaped(z=(z, x.shape), w=(w, (d,)), b=(b, (d,)))
-    y = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
-    kept = {}
-    if ckpt:
-        for name, t in (("x", x), ("z", z)):
-            if t is not None:
-                kept[name + "_codes"] = torch.empty((T, H, d), dtype=torch.float8_e4m3fn, device=x.device)
-                kept[name + "_exps"] = torch.empty(_exps_shape(T * H, d), dtype=torch.uint8, device=x.device)
-    gdn_norm_forward(x, z, w, b, y, kept.get("x_codes"), kept.get("x_exps"), kept.get("z_codes"),
-                     kept.get("z_exps"), T, H, d, _token_rows(x), H * d if z is None else _token_rows(z),
-                     H * d, eps, center, stream=stream)
+    with _gdn._on_stream(stream, x.device):
+        y = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
+        kept = {}
+        if ckpt:
+            for name, t in (("x", x), ("z", z)):
+                if t is not None:
+                    kept[name + "_codes"] = torch.empty((T, H, d), dtype=torch.float8_e4m3fn, device=x.device)
+                    kept[name + "_exps"] = torch.empty(_exps_shape(T * H, d), dtype=torch.uint8, device=x.device)
+        gdn_norm_forward(x, z, w, b, y, kept.get("x_codes"), kept.get("x_exps"), kept.get("z_codes"),
+                         kept.get("z_exps"), T, H, d, _token_rows(x), H * d if z is None else _token_rows(z),
+                         H * d, eps, center, stream=stream)
     return y, kept
 
 
@@ -267,17 +272,18 @@ def norm_backward(dy, x, w, z=None, b=None, x_exps=None, z_exps=None, eps=1e-6, 
     T, H, d = x.shape
     exps = _exps_shape(T * H, d)
     _shaped(dy=(dy, x.shape), z=(z, x.shape), w=(w, (d,)), b=(b, (d,)), x_exps=(x_exps, exps), z_exps=(z_exps, exps))
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dy.device)  # noqa: E731
-    g = dict(dx=new((T, H, d), dy.dtype), dw=new(d, torch.float32))
-    if z is not None:
-        g["dz"] = new((T, H, d), dy.dtype)
-    if b is not None:
-        g["db"] = new(d, torch.float32)
-    n = gdn_norm_workspace_bytes(T, H, d)
-    ws = new(n, torch.uint8) if n else None
-    gdn_norm_backward(x, x_exps, z, z_exps, w, b, dy, g["dx"], g.get("dz"), g["dw"], g.get("db"), T, H, d,
-                      _token_rows(x), H * d if z is None else _token_rows(z), _token_rows(dy), H * d, H * d,
-                      eps, center, workspace=ws, stream=stream)
+    with _gdn._on_stream(stream, dy.device):
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dy.device)  # noqa: E731
+        g = dict(dx=new((T, H, d), dy.dtype), dw=new(d, torch.float32))
+        if z is not None:
+            g["dz"] = new((T, H, d), dy.dtype)
+        if b is not None:
+            g["db"] = new(d, torch.float32)
+        n = gdn_norm_workspace_bytes(T, H, d)
+        ws = new(n, torch.uint8) if n else None
+        gdn_norm_backward(x, x_exps, z, z_exps, w, b, dy, g["dx"], g.get("dz"), g["dw"], g.get("db"), T, H, d,
+                          _token_rows(x), H * d if z is None else _token_rows(z), _token_rows(dy), H * d, H * d,
+                          eps, center, workspace=ws, stream=stream)
     return g
 
 
@@ -299,14 +305,15 @@ def chunk_backward(q, k, v, log_g, beta, dout, h0=None, dh_final=None, cu_seqlen
     _shaped(q_exps=(q_exps, _exps_shape(n * Hk, dk)), k_exps=(k_exps, _exps_shape(n * Hk, dk)),
             v_exps=(v_exps, _exps_shape(n * Hv, dv)))
     dt, dev = dout.dtype, dout.device
-    new = lambda shape, t=dt: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
-    g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dlog_g=new(log_g.shape), dbeta=new(beta.shape))
-    if h0 is not None if want_dh0 is None else want_dh0:
-        g["dh0"] = new(state, torch.float32)
-    io = GDN_E4M3 if _is_codes(q) else _code(q)
-    n = gdn_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, io, _code(dout), packed=cu_seqlens is not None)
-    ws = new(n, torch.uint8) if n else None
-    route = gdn_chunk_backward(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, dh_final, g["dq"],
-                               g["dk"], g["dv"], g["dlog_g"], g["dbeta"], g.get("dh0"), B, T, Hk, Hv, dk, dv,
-                               cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
+    with _gdn._on_stream(stream, dev):
+        new = lambda shape, t=dt: torch.empty(shape, dtype=t, device=dev)  # noqa: E731
+        g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dlog_g=new(log_g.shape), dbeta=new(beta.shape))
+        if h0 is not None if want_dh0 is None else want_dh0:
+            g["dh0"] = new(state, torch.float32)
+        io = GDN_E4M3 if _is_codes(q) else _code(q)
+        n = gdn_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, io, _code(dout), packed=cu_seqlens is not None)
+        ws = new(n, torch.uint8) if n else None
+        route = gdn_chunk_backward(q, k, v, q_exps, k_exps, v_exps, log_g, beta, h0, dout, dh_final, g["dq"],
+                                   g["dk"], g["dv"], g["dlog_g"], g["dbeta"], g.get("dh0"), B, T, Hk, Hv, dk, dv,
+                                   cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
     return g, route

@@ -212,3 +212,11 @@ def test_conveniences_refuse_shapes_they_would_read_beyond():
         gdn.norm_backward(x[:2], x, w)
     with pytest.raises(ValueError, match="must have shape"):
         gdn.ckpt8_load(torch.zeros(4, 130, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
+
+
+def test_a_stream_for_cpu_tensors_is_refused():
+    x, w = torch.zeros(4, 1, 128), torch.ones(128)
+    for call in (lambda: gdn.ckpt8_store(x, stream=16), lambda: gdn.norm_forward(x, w, stream=16),
+                 lambda: gdn.norm_backward(x, x, w, stream=16)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
