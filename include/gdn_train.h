@@ -147,7 +147,8 @@ int gdn_norm_backward_plan(const void* x, const uint8_t* x_exps, const void* z, 
  * either route.
  *
  * Limits: B, Hk, Hv, dk, dv >= 1, T >= 0, B and Hv <= 65535, Hv a multiple of
- * Hk, dk, dv <= 128; any finite gates with log_g <= 0.
+ * Hk, dk, dv <= 128; any finite gates with log_g <= 0 (one under -104, whose decay
+ * is zero in fp32, counts as -104).
  * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_HEAD_GROUPS,
  * GDN_ERR_DIM_LIMIT, GDN_ERR_DTYPE, GDN_ERR_WORKSPACE or GDN_ERR_HIP.
  */

@@ -130,7 +130,7 @@ __device__ __forceinline__ void load_gates(const Args& a, const ChunkAt& at, int
     if (tid < C) {
         const bool live = tid < at.rows;
         const int64_t r = (at.row0 + tid) * a.Hv + vh;
-        s->G[tid] = live ? (double)a.log_g[r] : 0.0;
+        s->G[tid] = live ? (double)bounded_log_decay(a.log_g[r]) : 0.0;   // (fp64 too has no digits left behind -1e38)
         s->beta[tid] = live ? a.beta[r] : 0.f;
     }
     __syncthreads();

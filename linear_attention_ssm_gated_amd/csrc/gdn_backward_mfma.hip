@@ -366,7 +366,7 @@ gdn_bwd_prep_kernel(Args a)
     if (w == 0) {
         const bool live = lane < at.rows;
         const int64_t r = (at.row0 + lane) * a.Hv + vh;
-        const float G = wave_scan(live ? a.log_g[r] : 0.f, lane) * kLog2e;
+        const float G = wave_scan(live ? bounded_log_decay(a.log_g[r]) : 0.f, lane) * kLog2e;
         const float GL = __shfl(G, 63);
         const float bt = live ? a.beta[r] : 0.f;
         sG[lane] = G;

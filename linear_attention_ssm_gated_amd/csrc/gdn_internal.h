@@ -8,6 +8,15 @@
 
 namespace gdn {
 
+// A log decay as the running sums of a chunk take it.  exp(-104) is zero in fp32
+// (below half of 2^-149), so that a stronger decay (a reset, down to the lowest
+// float) changes no decay factor by being taken as -104; as it stands it would take
+// the digits of every sum behind it, and the decays behind the reset are differences
+// of those sums.  Like this an fp32 sum behind one reset is rounded to 2^-18, behind
+// 63 of them to 2^-12, which is what a decay formed from it is off by, relative to
+// itself, for each rounding; weaker gates are taken as they are.  NaN stays NaN.
+__device__ __forceinline__ float bounded_log_decay(float g) { return g < -104.0f ? -104.0f : g; }
+
 // Arguments of one prefill call after host validation.
 struct PrefillArgs {
     const void* q;

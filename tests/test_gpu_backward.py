@@ -440,3 +440,17 @@ def test_gradient_against_differences():
     d1, d2 = ((loss(s) - loss(-s)) / (2 * s) for s in (h, h / 2))
     want = (4 * d2 - d1) / 3
     assert abs(got - want) <= 2e-3 * max(1.0, abs(want)), (got, want)
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g", [-104.0, -1e5, -1e6, -1e9, float(torch.finfo(torch.float32).min)])
+@pytest.mark.parametrize("at", ["once", "twelve a chunk", "every other token"])
+def test_resets_between_mild_gates(io, g, at):
+    # a gate that forgets everything, of any strength, among gates of about -0.07: the
+    # decays behind it are differences of sums that hold it
+    say("resets", io, g, at)
+    d = 128 if io == torch.bfloat16 else 32
+    inp = inputs(1, 130, 1, 2, d, d, io, True, True, seed=30)
+    rows = torch.tensor([20, 90]) if at == "once" else torch.arange(3, 130, 5 if at == "twelve a chunk" else 2)
+    inp["log_g"][0, rows] = g
+    check(inp, mfma=io == torch.bfloat16)
