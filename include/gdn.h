@@ -99,7 +99,8 @@ const char* gdn_last_route(void);
  *   allowed (updated in place).  q, k, v: io_dtype; out: out_dtype; log_g
  *   (natural log of the decay, <= 0, finite) and beta: fp32.  Any finite
  *   gates are taken: every decay factor either kernel forms is exp of a
- *   non-positive difference of cumulative log decays.
+ *   non-positive difference of cumulative log decays, in which a log_g under
+ *   -104, whose decay is zero in fp32, counts as -104.
  *
  * Kernels: io_dtype == GDN_BF16 with dk == dv == 128 and chunk == 64 runs the
  * bf16-MFMA spine (fp32 state and accumulators).  Every other accepted shape

@@ -84,7 +84,7 @@ gdn_prefill_generic_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
         }
         if (tid < L) {
             size_t off = (size_t)(row0 + t0 + tid) * Hv + vh;
-            sG[tid] = log_g[off];
+            sG[tid] = bounded_log_decay(log_g[off]);
             sB[tid] = beta[off];
         }
         __syncthreads();

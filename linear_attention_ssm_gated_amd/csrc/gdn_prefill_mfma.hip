@@ -350,7 +350,7 @@ gdn_wy_prep_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ 
         const rsrc_t rb_ = make_rsrc(beta + ru * Hv + vh, gb_bytes);
         const float gv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rg, (uint32_t)lane * Hv * 4u, 0, 0));
         const float bv = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rb_, (uint32_t)lane * Hv * 4u, 0, 0));
-        const float Gl2 = wave_scan_dpp(gv) * 1.4426950408889634f;
+        const float Gl2 = wave_scan_dpp(bounded_log_decay(gv)) * 1.4426950408889634f;
         sG[lane] = Gl2;
         sBt[lane] = bv;
         if (h < G) {

@@ -96,3 +96,21 @@ def test_generic_in_place_state():
     ro, rh = oracle_prefill(inp)
     assert rel_err(h, rh) <= TOL
     assert rel_err(out, ro) <= TOL
+
+
+@pytest.mark.parametrize("g", [-104.0, -1e6, -1e9, float(torch.finfo(torch.float32).min)])
+@pytest.mark.parametrize("step", [None, 13])
+def test_resets_between_mild_gates(g, step):
+    """Gates that forget everything, of any strength, among gates of about -0.07.
+    Behind n of them a sum of log decays is rounded to n 2^-18 at each of at most
+    64 / n additions: 2^-12 in all, were all errors of one sign; with random signs
+    2^-18 n sqrt(64 / n) / 3, 3e-5 for the five resets of a chunk."""
+    inp = synth.prefill_inputs(1, 150, 1, 2, 32, 32, io=torch.float32, h0=True, seed=906)
+    rows = torch.tensor([20, 100]) if step is None else torch.arange(3, 150, step)
+    inp["log_g"][0, rows] = g
+    say("generic resets", g, step)
+    out, hf, route = gpu_prefill(inp, 64)
+    assert "generic" in route, route
+    ro, rh = oracle_prefill(inp)
+    assert rel_err(out, ro) <= TOL
+    assert rel_err(hf, rh) <= TOL

@@ -243,3 +243,20 @@ def test_gates_from_the_ba_producer():
     assert route.startswith(ROUTE)
     assert torch.isfinite(out.float()).all() and torch.isfinite(hf).all()
     check(inp, out, hf)
+
+
+@pytest.mark.parametrize("g", [-104.0, -1e6, -1e9, float(torch.finfo(torch.float32).min)])
+@pytest.mark.parametrize("step", [None, 5, 2])
+@pytest.mark.parametrize("segmented", [False, True])
+def test_resets_between_mild_gates(g, step, segmented):
+    """A gate that forgets everything, of any strength, among gates of about
+    -0.07 (two of them, or every fifth or second token): the decays behind it are
+    differences of sums that hold it."""
+    inp = synth.prefill_inputs(1, 300, 2, 6, 128, 128, h0=True, seed=905)
+    rows = torch.tensor([20, 150]) if step is None else torch.arange(3, 300, step)
+    inp["log_g"][0, rows] = g
+    say("resets", g, step, segmented)
+    out, hf, route = gpu_prefill(inp, 64, segmented=segmented)
+    assert route.startswith("gdn_wy_prep_kernel"), route
+    assert torch.isfinite(out.float()).all() and torch.isfinite(hf).all()
+    check(inp, out, hf)
