@@ -216,7 +216,8 @@ int gdn_chunk_prefill_segmented_plan(const void* q, const void* k, const void* v
  *   h_table[b]: device pointer to sequence b's states [Hv][dk][dv] fp32
  *   stash: sequence b at stash + b*stash_seq_floats; per v-head vh, at
  *          vh*(K*dv + K + kfl) floats: delta [K][dv] fp32, G [K] fp32 (the
- *          within-verify cumulative log decay), then the K keys [K][dk] as
+ *          within-verify cumulative log decay, a gate under -104, whose decay
+ *          is zero in fp32, counting as -104), then the K keys [K][dk] as
  *          kfl = K*dk floats (fp32 io) or ceil(K*dk/2) floats of packed bf16
  *          bits (bf16 io).  The fold receives no q/k/v/gate, so the stash
  *          carries them.

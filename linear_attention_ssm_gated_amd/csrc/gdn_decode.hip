@@ -76,7 +76,7 @@ gdn_verify_kernel(float* const* __restrict__ h_table, const TIn* __restrict__ q,
     }
     if (tid < KR) {
         const size_t off = ((size_t)b * KR + tid) * gb_stride + vh;
-        sG[tid] = gate[off];
+        sG[tid] = bounded_log_decay(gate[off]);
         sBeta[tid] = beta[off];
     }
     __syncthreads();
@@ -406,7 +406,7 @@ gdn_verify_d128_kernel(float* const* __restrict__ h_table, const TIn* q, const T
             else { sk[r][i] = x; sk2[r][i2] = x; }
         }
     }
-    if (tid < KR) { sG[tid] = g_in; sBeta[tid] = b_in; }
+    if (tid < KR) { sG[tid] = bounded_log_decay(g_in); sBeta[tid] = b_in; }
     __syncthreads();
 
     // k_r . k_s and q_r . k_s: pair tid/16 (+ 16 per round) sums elements

@@ -364,3 +364,18 @@ def test_two_steps_equal_the_two_row_chunk(dk):
     got = torch.stack([x for x in s.slots]).cpu()
     for b in range(4):
         assert rel_err(got[b], after[b, 2]) <= 1e-4, b
+
+
+@pytest.mark.parametrize("g", [-104.0, -1e6, -1e9, float(torch.finfo(torch.float32).min)])
+@pytest.mark.parametrize("rows", [[2], [0, 5], [1, 3, 4, 6]])
+@pytest.mark.parametrize("d", [128, 64])
+def test_resets_between_mild_gates(g, rows, d):
+    """A gate that forgets everything, of any strength, among gates of about
+    -0.07: the decays of the rows behind it are differences of sums that hold it,
+    in the verify and, from the stash, in the fold.  Behind four of them the sums
+    are rounded to 2^-16 an addition, so 1e-4 stands."""
+    inp = synth.decode_inputs(5, 8, 1, 3, d, d, io=torch.bfloat16, seed=390 + d)
+    inp["gate"][:, rows] = g
+    say("verify resets", g, rows, d)
+    s = Setup(inp, torch.bfloat16, torch.float32)
+    check_verify_fold(inp, s, "gdn_verify_d128_kernel" if d == 128 else "gdn_verify_kernel", 1e-4)
