@@ -236,7 +236,8 @@ __device__ __forceinline__ float normalise(float* x, const Shape& s, int l, floa
     } else {
         q = row_sum<TPR>(q, red, 1) * s.inv_d;
     }
-    return __builtin_amdgcn_rsqf(fmaxf(q, 0.f) + s.eps);
+    // (a centred row's may round below zero; fmaxf would make a NaN row's zero too)
+    return __builtin_amdgcn_rsqf((q < 0.f ? 0.f : q) + s.eps);
 }
 
 // Codes and scale byte of the VEC = 8 values of each lane, a group's 128 lying

@@ -207,3 +207,24 @@ def test_heads_of_one_token_past_32_bits():
     rows = gdn.norm_backward(dy.view(H, 1, d), x.view(H, 1, d), w, z=x.view(H, 1, d))
     for n in one:
         assert torch.equal(one[n].flatten(), rows[n].flatten()), n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("center,bad", [(False, "nan"), (True, "nan"), (True, "inf")])
+@pytest.mark.parametrize("d", [128, 100, 2048, 4099])
+def test_a_bad_row_is_nan(dtype, center, bad, d):
+    # the statistics of a row that holds a NaN are NaN, and so is all that they
+    # enter: the row's y, dx and dz, and dw; of a centred row, whose mean is then
+    # infinite or NaN, with an infinity too
+    say("norm bad row", dtype, center, bad, d)
+    c = make(9, 2, d, dtype, gate=True, bias=False, seed=3)
+    c["x"][4, 1, 7] = float(bad)
+    x, z, w, dy = on(c["x"]), on(c["z"]), on(c["w"]), on(c["dy"])
+    y, kept = gdn.norm_forward(x, w, z=z, center=center, ckpt=True)
+    g = gdn.norm_backward(dy, x, w, z=z, center=center)
+    h = gdn.norm_backward(dy, kept["x_codes"], w, z=kept["z_codes"], x_exps=kept["x_exps"], z_exps=kept["z_exps"], center=center)
+    rows = torch.zeros(9, 2, dtype=torch.bool)
+    rows[4, 1] = True
+    for t in (y, g["dx"], g["dz"], h["dx"], h["dz"]):
+        assert bool(torch.isnan(t.cpu()[rows]).all()) and not bool(torch.isnan(t.cpu()[~rows]).any())
+    assert bool(torch.isnan(g["dw"]).all()) and bool(torch.isnan(h["dw"]).all())
