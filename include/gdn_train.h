@@ -44,6 +44,10 @@ extern "C" {
  * and one e4m3 code per value, codes[r * d + j], the value over the scale
  * rounded to nearest even; infinities and NaN become the NaN code.  A code
  * times its scale is exactly a bf16 value, down to bf16's own smallest.
+ * Groups whose largest magnitude is above 448 * 2^119 have byte 247, which
+ * stands for 255 * 2^112 instead of 2^120: like this the largest finite value's
+ * code, 256, is bf16's largest finite value and not infinity.  A code times that
+ * one scale has 12 bits, and is rounded where bf16 takes it.
  *
  * store: x [rows][x_stride] (io_dtype F32 or BF16) -> codes, exps.
  * load:  codes, exps -> y [rows][y_stride] (out_dtype F32 or BF16).

@@ -102,9 +102,20 @@ __device__ __forceinline__ int ckpt_exp_byte(float top)
     byte = byte < 1 ? 1 : byte;
     return u == 0 ? 127 : byte;
 }
-// 2^(byte - 127) for bytes 1..246, and its reciprocal
-__device__ __forceinline__ float ckpt_scale(int byte) { return __uint_as_float((uint32_t)byte << 23); }
-__device__ __forceinline__ float ckpt_inverse(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+// 2^(byte - 127) for bytes 1..246, and its reciprocal.  The last byte, 247, stands for
+// 255 2^112 instead of 2^120: the largest float is 256.99 of it and rounds to code 256,
+// which is 255 2^120, bf16's largest finite value, where 256 2^120 would be infinity.
+// (A select; bringing back the one code behind the product took 4 to 8 us of the
+// 274 of a packed backward call from codes.)
+constexpr int kCkptTopByte = 247;
+__device__ __forceinline__ float ckpt_scale(int byte)
+{
+    return byte == kCkptTopByte ? 0x1.fep119f : __uint_as_float((uint32_t)byte << 23);
+}
+__device__ __forceinline__ float ckpt_inverse(int byte)
+{
+    return byte == kCkptTopByte ? 0x1.010102p-120f : __uint_as_float((uint32_t)(254 - byte) << 23);
+}
 
 // |x| where finite, 0 for infinities and NaN
 __device__ __forceinline__ float ckpt_magnitude(float x)

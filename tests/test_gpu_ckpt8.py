@@ -81,3 +81,63 @@ def test_round_trip_error_and_no_rows():
     c, e = gdn.ckpt8_store(torch.empty((0, 128), device=dev()))
     assert c.shape == (0, 128) and e.shape == (0, 1)
     assert gdn.ckpt8_load(c, e).shape == (0, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d,pad", [(128, 0), (256, 0), (100, 0), (130, 1)])
+def test_the_largest_finite_values_come_back_finite(dtype, d, pad):
+    # the last binade: byte 247, codes up to 256
+    say("ckpt8 largest values", dtype, d, pad)
+    x = torch.linspace(1.0, 2.0 - 2.0 ** -7, 5 * d).reshape(5, d).mul(2.0 ** 127).to(dtype)
+    x[:, 1::2] /= 200.0
+    x[:, 0] = torch.finfo(dtype).max
+    x[:, d - 1] = -torch.finfo(dtype).max
+    x[2, 3], x[2, 4] = float("nan"), float("inf")
+    codes, exps = gdn.ckpt8_store(x.to(dev()))
+    assert bool((exps == 247).all())
+    y = torch.full((5, d + pad), 7.0, dtype=torch.float32, device=dev())
+    gdn.gdn_ckpt8_load(codes, exps, y, 5, d, d + pad)
+    got, ref = y[:, :d].cpu().double(), x.double()
+    ok = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got), ok) and bool(torch.isnan(got[~ok]).all())
+    # half a step, and the roundings of the reciprocal and of the product with it
+    assert bool(((got - ref).abs()[ok] <= (2.0 ** -4 + 2.0 ** -22) * ref.abs()[ok]).all())
+    vals = train_ref.e4m3_values()[codes.view(torch.uint8).cpu().numpy()] * 255.0 * 2.0 ** 112
+    assert np.array_equal(vals[ok.numpy()], got.numpy()[ok.numpy()])
+    half = gdn.ckpt8_load(codes, exps, torch.bfloat16).cpu()
+    assert torch.equal(half.double().nan_to_num(), got.to(torch.float32).to(torch.bfloat16).double().nan_to_num())
+
+
+@pytest.mark.parametrize("d", [128, 100])
+def test_the_backward_passes_read_the_largest_values_alike(d):
+    # the gradients from codes of byte 247 are those of the values that
+    # gdn_ckpt8_load gives, to the bit
+    say("ckpt8 largest values, read by the backward passes", d)
+    gen = torch.Generator().manual_seed(d)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    big = lambda t: t.sign() * (1.9 + 0.09 * torch.rand(t.shape, generator=gen)) * 2.0 ** 127  # noqa: E731
+    on = lambda t: t.to(dev())  # noqa: E731
+    x, z, dy, w = r(6, 2, d), big(r(6, 2, d)).abs(), r(6, 2, d) * 2.0 ** -100, r(d)
+    xc, xe = gdn.ckpt8_store(on(x))
+    zc, ze = gdn.ckpt8_store(on(z))
+    assert int(ze.min()) == 247
+    a = gdn.norm_backward(on(dy), xc, on(w), z=zc, x_exps=xe, z_exps=ze)
+    b = gdn.norm_backward(on(dy), gdn.ckpt8_load(xc, xe, torch.float32), on(w), z=gdn.ckpt8_load(zc, ze, torch.float32))
+    for n in a:
+        assert bool(torch.isfinite(a[n]).all()) and torch.equal(a[n], b[n]), n
+    q, k, v = r(1, 70, 1, d) / d ** 0.5, r(1, 70, 1, d) / d ** 0.5, r(1, 70, 2, d)
+    v[0, 30] = big(v[0, 30])
+    gate, beta = on(torch.full((1, 70, 2), -0.1)), torch.full((1, 70, 2), 0.5)
+    beta[0, 30] = 2.0 ** -120
+    dt = torch.bfloat16 if d == 128 else torch.float32
+    dout = on((r(1, 70, 2, d) * 2.0 ** -20).to(dt))
+    kept = [gdn.ckpt8_store(on(t)) for t in (q, k, v)]
+    vals = [gdn.ckpt8_load(*t, dt) for t in kept]
+    assert int(kept[2][1].max()) == 247 and all(bool(torch.isfinite(t).all()) for t in vals)
+    a, route = gdn.chunk_backward(*(t[0] for t in kept), gate, on(beta), dout, q_exps=kept[0][1], k_exps=kept[1][1],
+                                  v_exps=kept[2][1])
+    assert route.startswith("gdn_bwd_prep" if d == 128 else "gdn_backward_prep"), route
+    b, _ = gdn.chunk_backward(*vals, gate, on(beta), dout)
+    for n in a:
+        assert bool(torch.isfinite(a[n].float()).all()), n
+        assert torch.equal(a[n], b[n]), n
