@@ -434,10 +434,12 @@ gdn_norm_backward_kernel(const A* __restrict__ x, const uint8_t* __restrict__ x_
                 const float n = xv[c] * r;
                 xv[c] = n;
                 if constexpr (GATE) {
-                    // silu' = s + z s (1 - s) = s + silu - silu s
+                    // silu' = s + z s (1 - s); where s rounds to 1 the second term is
+                    // zero at once (z s - z s s, with s added to z s, loses the s
+                    // beside a large z)
                     const float sg = sigmoid(zv[c]), d = gv[c], si = zv[c] * sg;
                     gv[c] = d * si;
-                    o[e] = d * fmaf(n, wv[c], bv[c]) * fmaf(-si, sg, sg + si);
+                    o[e] = d * fmaf(n, wv[c], bv[c]) * fmaf(si, 1.0f - sg, sg);
                 }
                 dw[c] = fmaf(gv[c], n, dw[c]);
             }

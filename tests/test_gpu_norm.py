@@ -228,3 +228,19 @@ def test_a_bad_row_is_nan(dtype, center, bad, d):
     for t in (y, g["dx"], g["dz"], h["dx"], h["dz"]):
         assert bool(torch.isnan(t.cpu()[rows]).all()) and not bool(torch.isnan(t.cpu()[~rows]).any())
     assert bool(torch.isnan(g["dw"]).all()) and bool(torch.isnan(h["dw"]).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gates_of_any_size(dtype):
+    # silu'(z) = s + z s (1 - s) goes to 1 for a large z.  s and 1 - s are off by 2^-22
+    # at the most and 1 - s is exactly zero from z = 18 on, so that z s (1 - s) is off
+    # by 18 * 2^-22 = 4e-6, beside values of s of 1
+    say("norm large gates", dtype)
+    c = make(8, 2, 128, dtype, gate=True, bias=True, seed=9)
+    for i, v in enumerate([5.0, 12.0, 17.0, 50.0, 1e3, 1e5, 1e8, 1e30]):
+        c["z"][i] = (torch.ones(2, 128) * v).to(dtype)
+    g = gdn.norm_backward(on(c["dy"]), on(c["x"]), on(c["w"]), z=on(c["z"]), b=on(c["b"]))
+    ref = train_ref.norm_grads(c["dy"], c["x"], c["w"], c["z"], c["b"])["dz"]
+    d = (g["dz"].cpu().double() - ref).abs()
+    step = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    assert bool((d <= (step + 1e-5) * ref.abs() + 1e-5 * ref.abs().amax(-1, keepdim=True)).all())
