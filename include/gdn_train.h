@@ -52,8 +52,8 @@ extern "C" {
  * store: x [rows][x_stride] (io_dtype F32 or BF16) -> codes, exps.
  * load:  codes, exps -> y [rows][y_stride] (out_dtype F32 or BF16).
  * codes [rows][d] and exps are dense.  rows >= 0 (0 launches nothing);
- * d >= 1; a stride >= d.  Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE,
- * GDN_ERR_DTYPE, GDN_ERR_STRIDE or GDN_ERR_HIP.
+ * 1 <= d <= 2^30; a stride >= d.  Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE,
+ * GDN_ERR_DIM_LIMIT (d), GDN_ERR_DTYPE, GDN_ERR_STRIDE or GDN_ERR_HIP.
  */
 int gdn_ckpt8_store(const void* x, uint8_t* codes, uint8_t* exps, int64_t rows, int d,
                     int64_t x_stride, int io_dtype, hipStream_t stream);

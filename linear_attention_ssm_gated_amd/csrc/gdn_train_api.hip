@@ -38,6 +38,7 @@ int check_ckpt(const gdn::CkptArgs& a, bool store)
     const char* who = store ? "gdn_ckpt8_store" : "gdn_ckpt8_load";
     if (!wide_dtype(a.dtype)) return refuse_call(GDN_ERR_DTYPE, who, "dtype must be GDN_F32 or GDN_BF16");
     if (a.rows < 0 || a.d < 1) return refuse_call(GDN_ERR_SHAPE, who, "need rows >= 0 and d >= 1");
+    if (a.d > (1 << 30)) return refuse_call(GDN_ERR_DIM_LIMIT, who, "d <= 2^30");
     if (a.stride < a.d) return refuse_call(GDN_ERR_STRIDE, who, "a row stride is shorter than its row");
     const bool all = store ? a.x && a.codes && a.exps_out : a.x && a.exps_in && a.y;
     if (a.rows > 0 && !all)

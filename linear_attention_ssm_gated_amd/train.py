@@ -210,6 +210,14 @@ def _shaped(**want):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _row_width(t):
+    """Width of t's rows, which the C call takes as an int."""
+    d = t.shape[-1]
+    if d > 1 << 30:
+        raise ValueError("a row has at most 2^30 values: give a long tensor rows")
+    return d
+
+
 def _exps_shape(rows, d):
     return rows, -(-d // CKPT8_GROUP)
 
@@ -227,7 +235,7 @@ def ckpt8_store(x, stream=None):
     float8_e4m3fn of x's shape, exps uint8 [rows, ceil(d / 128)])."""
     if not x.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    d = x.shape[-1]
+    d = _row_width(x)
     rows = x.numel() // d if d else 0
     with _gdn._on_stream(stream, x.device):
         codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
@@ -238,7 +246,7 @@ def ckpt8_store(x, stream=None):
 
 def ckpt8_load(codes, exps, dtype=torch.bfloat16, stream=None):
     """The values of an 8-bit checkpoint as a tensor of codes' shape."""
-    d = codes.shape[-1]
+    d = _row_width(codes)
     rows = codes.numel() // d if d else 0
     _shaped(exps=(exps, _exps_shape(rows, d)))
     with _gdn._on_stream(stream, codes.device):

@@ -141,3 +141,16 @@ def test_the_backward_passes_read_the_largest_values_alike(d):
     for n in a:
         assert bool(torch.isfinite(a[n].float()).all()), n
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_one_long_row(off):
+    # the widest row: its groups are those of the same values in rows of 128, with
+    # wide loads (off = 0) and value by value
+    say("ckpt8 long row", off)
+    n = 1 << 30
+    x = torch.empty(n + 1, dtype=torch.bfloat16, device=dev())[off:off + n].normal_(generator=torch.Generator(dev()).manual_seed(6))
+    codes, exps = gdn.ckpt8_store(x)
+    c, e = gdn.ckpt8_store(x.clone().view(-1, 128))
+    assert torch.equal(codes.view(torch.uint8), c.view(torch.uint8).flatten()) and torch.equal(exps.flatten(), e.flatten())
+    assert torch.equal(gdn.ckpt8_load(codes, exps), gdn.ckpt8_load(c, e).flatten())

@@ -220,3 +220,17 @@ def test_a_stream_for_cpu_tensors_is_refused():
                  lambda: gdn.norm_backward(x, x, w, stream=16)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_rows_of_more_than_2_30_values_are_refused(lib):
+    # (a group's and a column's number are formed in 32 bits)
+    for d in ((1 << 30) + 1, (1 << 31) - 64, (1 << 31) - 1):
+        assert store(lib, rows=1, d=d, stride=1 << 33) == S["GDN_ERR_DIM_LIMIT"], gdn.last_route()
+        assert load(lib, rows=1, d=d, stride=1 << 33) == S["GDN_ERR_DIM_LIMIT"], gdn.last_route()
+    assert store(lib, rows=1, d=1 << 30, stride=1 << 30) == 0
+    # an int of the C call would wrap: 2^32 + 128 values of one row would be 128
+    x = torch.empty((1 << 32) + 128, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^30"):
+        gdn.ckpt8_store(x)
+    with pytest.raises(ValueError, match="2\\^30"):
+        gdn.ckpt8_load(x.to(torch.uint8), torch.empty((1, 1), dtype=torch.uint8, device="meta"))
