@@ -843,13 +843,12 @@ hipError_t launch_walk(const Args& k, unsigned chunks, hipStream_t s)
 
 }  // namespace
 
-size_t backward_generic_workspace_bytes(const BackwardArgs& a) { return layout(a).total; }
-
 size_t backward_workspace_need(const BackwardArgs& a)
 {
-    // the generic route's is the larger one, and an unaligned call of the MFMA
-    // route's types falls back to it
-    return backward_generic_workspace_bytes(a);
+    // the generic route's, which a call of the MFMA route's types takes too where a
+    // pointer is not aligned; at 128 x 128 it is the larger one (304 KiB and more a
+    // chunk and v-head, the MFMA route's 138 KiB)
+    return layout(a).total;
 }
 
 Geometry backward_generic_geometry(const BackwardArgs& a)

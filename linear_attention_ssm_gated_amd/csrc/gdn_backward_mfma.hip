@@ -7,12 +7,18 @@
 //   grads   one workgroup per (chunk, k-head): the gradients of the chunk, the
 //           v-heads of the k-head in turn, dq and dk summed in registers (short
 //           calls: one per v-head, and a sum over the k-head's)
-// 4576 tokens of 16 / 48 heads in bf16 take 466 us back to back (prep 95, spine
-// 164, grads 240), where the inputs and gradients alone would take 48 us at a large
-// copy's rate and the products 64 us at a large matrix product's; the generic route
-// takes 3.0 ms.  Matrices are rounded to bf16 where a product takes them (T, P, W,
-// U, Qt; h and dh' from their fp32 states; u, dx and the masked products), as the
-// matrix units need; sums, states, gates and statistics stay fp32.
+// 4576 tokens of 16 / 48 heads in bf16 take 466 us back to back (traced, which slows
+// each kernel a little: prep 91 to 92, spine 159, grads 231 to 233), where the inputs and gradients
+// alone would take 48 us at a large copy's rate and the products 64 us at a large
+// matrix product's; the generic route takes 2.8 ms.  The matrices that the three hand
+// on set a floor of their own: 1482 MB moved, 288 us at a copy's rate.
+// Matrices are rounded to bf16 where a product takes them (T, P, W, U, Qt; h and dh',
+// which the gradients read as such; u, dx and the masked products), as the matrix units
+// need; the walked states, sums, gates and statistics stay fp32.  Of an error of 3.3e-3
+// in the 2-norm the outputs' own rounding is 1.7e-3; P, x = V - ga K h, u, beta ddelta
+// and dP o Gam add 1.2e-3 to 1.7e-3 each to the gradients behind them, all others under
+// 6e-4 (each rounded alone in 64 bits).  dlog_g's sums take B, P, h and dh' as rounded:
+// fp32 copies of h and dh' beside the bf16 ones would move 906 MB more for 5e-4 of it.
 //
 // Operands.  v_mfma_f32_16x16x32_bf16: lane 16 g + n supplies A[n][8g .. 8g+7]
 // and B[8g .. 8g+7][n] of a 32-wide k-step and holds rows 4g .. 4g+3 of column
@@ -310,7 +316,7 @@ extern __shared__ __attribute__((aligned(1024))) byte lds[];
 // Four waves, two workgroups a compute unit.  T by 16 x 16 blocks in fp32; P diag(beta)
 // T, W, U and Qt are products with T's and (P beta T ga)'s columns as they lie
 // transposed in LDS.  Bound by the workspace it writes: 4576 tokens, 48 v-heads: 263
-// MB written and 103 MB read (counters) in 95 us, 3.9 TB/s.
+// MB written and 106 MB read (counters) in 91 to 92 us, 4.0 TB/s.
 using bwd::kBP;                                // pitch of the fp32 matrix B
 constexpr int P_K = 0;                         // K
 constexpr int P_Q = P_K + kTile;               // Q, then V
@@ -519,8 +525,8 @@ gdn_bwd_prep_kernel(Args a)
 // two products follow each other in its registers.  Four load: the next chunks'
 // matrices through registers (three steps ahead) into the LDS stage that is not
 // being read, so that a load or an LDS write that waits for the compute unit's
-// memory path holds up no product.  72 steps of 48 v-heads take 164 us (315 MB read
-// and 226 MB written by the counters, 3.3 TB/s), 197 us with four waves that did
+// memory path holds up no product.  72 steps of 48 v-heads take 159 us (316 MB read
+// and 226 MB written by the counters, 3.4 TB/s), 197 us with four waves that did
 // both and without the XCD order of Walk.  A step's latency is the time: 4800 cycles
 // backwards, of which the products fill 770, the LDS reads about 2000 and the 72 KB
 // of matrices through the compute unit's memory path 2200.  Loading waves that also
@@ -755,14 +761,15 @@ gdn_bwd_spine_kernel(Args a)
 // ---- grads -------------------------------------------------------------------------
 // Eight waves, two to a SIMD, so that one's products run under the other's vector
 // work and LDS reads; the LDS holds a v-head whole (K, Q, do, V, h, dh', T, P), so one
-// workgroup a compute unit.  72 x 16 chunks and k-heads of three v-heads: 240 us (471
-// MB read, 100 MB written by the counters, 2.4 TB/s).  Nothing is full: LDS 35 % of
+// workgroup a compute unit.  72 x 16 chunks and k-heads of three v-heads: 231 to 233 us (471
+// MB read, 100 MB written by the counters, 2.5 TB/s).  Nothing is full: LDS 35 % of
 // the cycles (a third more in bank conflicts), vector units 35 %, matrix units 14 %;
 // the time is the five barriers of a v-head, each behind a chain of reads, products
-// and rounding, and 4.5 rounds of workgroups, the last half empty.  Taken and dropped: four
+// and rounding, and 4.5 rounds of workgroups, the last half empty; the matrices that it
+// reads would take 111 us at a large copy's rate.  Taken and dropped: four
 // waves with the next v-head in registers (250 us), eight with it (250 to 270 us, as
 // registers spill), h, dh', T and P by asynchronous loads to LDS under the last products
-// (234 to 239 us: the loads' time moves into the phases that they run under).
+// (no gain: the loads' time moves into the phases that they run under).
 constexpr int kGradThreads = 512;
 constexpr int G_K = 0;
 constexpr int G_Q = G_K + kTile;
@@ -1325,8 +1332,6 @@ const char* backward_mfma_refuses(const BackwardArgs& a)
         return "(generic: the MFMA route takes 16-byte aligned pointers)";
     return nullptr;
 }
-
-size_t backward_mfma_workspace_bytes(const BackwardArgs& a) { return layout(a.B, a.T, a.Hv, a.cu != nullptr).total; }
 
 Geometry backward_mfma_geometry(const BackwardArgs& a)
 {

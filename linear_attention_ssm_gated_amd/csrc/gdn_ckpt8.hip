@@ -7,7 +7,7 @@
 // 2^-9 of 448 * 2^-e below), needs one byte, and leaves every decoded value
 // exactly representable in bf16, so that a bf16 matrix product takes it
 // without a second rounding.  The code is rounded to nearest even: relative
-// error at most 2^-4.
+// error at most 2^-4.  (The last scale byte is not a power of two: ckpt_scale.)
 //
 // Both kernels are bound by HBM: store moves (element size + 1) bytes a value
 // in one pass, the group's maximum formed in registers across the 8 lanes

@@ -161,7 +161,8 @@ template <int TPR> __device__ __forceinline__ void row_sum2(float& x, float& y, 
 
 // The hardware's exp2 and reciprocal, within one unit in the last place each: a
 // relative error of a few 2^-24, far below the output's rounding to bf16 and
-// without the instructions of a correctly rounded division.
+// without the instructions of a correctly rounded division.  (fp32 gradients are off
+// by 1.1e-7 in the 2-norm, 5.8e-8 for a form in fp32 that rounds each step once.)
 __device__ __forceinline__ float sigmoid(float z)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));

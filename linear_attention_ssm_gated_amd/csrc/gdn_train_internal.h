@@ -71,8 +71,6 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s);
 // Bytes either route needs for these sizes and types (pointers are only
 // compared with NULL).
 size_t backward_workspace_need(const BackwardArgs& a);
-size_t backward_generic_workspace_bytes(const BackwardArgs& a);
-size_t backward_mfma_workspace_bytes(const BackwardArgs& a);
 // The guard that keeps a call off the MFMA route, NULL where it takes it.
 const char* backward_mfma_refuses(const BackwardArgs& a);
 Geometry backward_mfma_geometry(const BackwardArgs& a);
