@@ -232,8 +232,8 @@ def gdn_fold(h_table, stash, na_tab, hi_tables, slab_entries, engaged_flag, k_ro
 
 # ---- allocation conveniences (torch allocates, the library computes) ------
 # With stream= a convenience behaves like a torch operator under
-# torch.cuda.stream(stream): its outputs belong to that stream, and another
-# stream waits before it reads them.
+# torch.cuda.stream(stream): the caller has that stream wait for what writes the
+# inputs, the outputs belong to it, and another stream waits before it reads them.
 
 def gdn_ba_gates_workspace_bytes(m, n, k) -> int:
     return library().gdn_ba_gates_workspace_bytes(m, n, k)
