@@ -8,7 +8,9 @@ hardware's exp2, 2^-23), c by 2^-20 (a polynomial and a square root of values th
 are each off by a few 2^-23, over 1 - a >= 0.22 where it is a difference), the
 multiply-add by 2^-24.  So E_t = a_t E_{t-1} + ((4 + |l|) 2^-23 + 2^-20 [c]) S_t
 bounds the row by row form.  Composing runs of rows adds one rounding of S_t's size
-for each run that lies between, and at most 64 + rows / 128 lie there."""
+for each run that lies between: at most 16 in a segment and one for each segment before
+it, which have 96 rows at least, or 64 under 8 channels.  64 + rows / 128 is as much for
+all up to 6144 rows."""
 from __future__ import annotations
 
 import torch
@@ -28,6 +30,10 @@ def coefficients(l, scale):
     return a, c, torch.where(c > 0, -a * a / c, torch.zeros_like(c))
 
 
+def runs_between(rows, D):
+    return max(64 + rows / 128, 16 + rows / (64 if D < 8 else 96))
+
+
 def spans(B, T, cu):
     if cu is None:
         return [(b * T, (b + 1) * T) for b in range(B)]
@@ -45,7 +51,7 @@ def forward(x, log_a, h0, seqs, scale):
     for b, (s, e) in enumerate(seqs):
         h = torch.zeros(D, dtype=F64) if h0 is None else h0[b].to(F64)
         S, E = h.abs(), torch.zeros(D, dtype=F64)
-        joins = (64 + (e - s) / 128) * 2.0 ** -24
+        joins = runs_between(e - s, D) * 2.0 ** -24
         for t in range(s, e):
             h = a[t] * h + c[t] * x[t]
             S = a[t] * S + (c[t] * x[t]).abs()
@@ -70,7 +76,7 @@ def backward(x, log_a, y, h0, dy, dht, seqs, scale):
     for b, (s, e) in enumerate(seqs):
         G = torch.zeros(D, dtype=F64) if dht is None else dht[b].to(F64)
         S, E = G.abs(), torch.zeros(D, dtype=F64)
-        joins = (64 + (e - s) / 128) * 2.0 ** -24
+        joins = runs_between(e - s, D) * 2.0 ** -24
         for t in reversed(range(s, e)):
             g = dy[t] + G
             M, Eg = dy[t].abs() + S, E + (joins + 2.0 ** -24) * (dy[t].abs() + S)
