@@ -111,10 +111,11 @@ template <int V> __device__ __forceinline__ void store_vec(uint16_t* p, const fl
 }
 
 // a = exp(l), and with an input scale u = 1 - a with its own digits: sqrt(1 - a^2) =
-// sqrt((1 - a)(1 + a)) is formed from it.  Near 0, for -1/8 < l < 0, 1 - a is
-// -expm1(l) by its Taylor polynomial (the first term left out is l^5 / 720 of l, 4e-8 at
-// -1/8); else a is off by (2 + |l|) 2^-23 of itself, and 1 - a, at least 0.117, by 2^-20 of
-// itself at most.  S: 0 plain, 1 complement, 2 root.
+// sqrt((1 - a)(1 + a)) is formed from it.  Near 0, for -1/4 < l < 0, 1 - a is -expm1(l) =
+// -(l + l^2 p(l)), p the cubic whose largest error there, relative to expm1, is least (2^-28,
+// with its coefficients rounded; the Taylor polynomial of as many terms is 2^-19 off at -1/4):
+// 1 - a within 1.5 2^-24 of itself.  Else a is off by (2 + |l|) 2^-23 of itself, and 1 - a, at
+// least 0.22, by 2^-20 of itself at most.  S: 0 plain, 1 complement, 2 root.
 template <int S> struct Decay {
     float a, u;
     __device__ __forceinline__ explicit Decay(float l)
@@ -124,11 +125,11 @@ template <int S> struct Decay {
             a = far;
             u = 1.0f;
         } else {
-            float q = fmaf(l, 1.0f / 120, 1.0f / 24);
-            q = fmaf(l, q, 1.0f / 6);
-            q = fmaf(l, q, 0.5f);
+            float q = fmaf(l, 0x1.ed7c28p-8f, 0x1.53f7d6p-5f);
+            q = fmaf(l, q, 0x1.554e1ap-3f);
+            q = fmaf(l, q, 0x1.ffffe8p-2f);
             q = fmaf(l * l, q, l);
-            const bool near = __float_as_uint(l) - 0x80000000u < 0x3e000000u;
+            const bool near = __float_as_uint(l) - 0x80000000u < 0x3e800000u;
             a = near ? 1.0f + q : far;
             u = near ? -q : 1.0f - far;
         }
