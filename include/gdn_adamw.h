@@ -40,7 +40,9 @@ typedef struct gdn_adamw_tensor {
  *   w <- (1 - lr weight_decay) w - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in fp32, each operation rounded by itself (no fused multiply-add), so that the
  * result is that of the same operations one by one; with GDN_E4M3 states the
- * quotient m / (...) is within 2^-22 of itself instead.
+ * quotient m / (...) is a division's save for one in a million, which rounds to the
+ * float next to it, and for BF16 weights without master, which are rounded to 2^-9
+ * at once, within 2^-22 of itself.
  *
  * state_dtype GDN_F32: m and v are kept as they are.  GDN_E4M3: the first moment
  * and the root of the second are each kept as e4m3 codes with one fp32 scale per
