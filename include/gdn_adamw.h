@@ -70,7 +70,8 @@ typedef struct gdn_adamw_tensor {
  * Any alignment of the element types; tensors must not overlap.  count >= 0
  * tensors; up to 64 (8-bit states: 48) of them go into one launch.
  * Limits: n <= 2^40, step >= 1, 0 <= beta < 1, eps >= 0 (with GDN_E4M3 states 0 or
- * at least 2^-126); eps, lr and grad_factor finite in fp32.
+ * at least 2^-126); eps, lr, grad_factor, lr / (1 - beta1^step) and each
+ * 1 - lr weight_decay finite in fp32 (of a control's words nothing is checked).
  * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE or GDN_ERR_HIP.
  */
 int gdn_adamw_step(const gdn_adamw_tensor* tensors, int count, double lr, double beta1, double beta2,

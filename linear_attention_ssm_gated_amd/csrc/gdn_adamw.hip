@@ -372,6 +372,10 @@ struct Call {
     uint32_t seed;
 };
 
+// what the kernel multiplies by, in fp32
+float rate_of(const Call& a) { return (float)(a.lr / (1 - pow(a.beta1, (double)a.step))); }
+float decay_of(const Call& a, const gdn_adamw_tensor& t) { return (float)(1.0 - a.lr * (double)t.weight_decay); }
+
 int check(const Call& a)
 {
     const char* who = "gdn_adamw_step";
@@ -388,6 +392,8 @@ int check(const Call& a)
         return refuse_call(GDN_ERR_SHAPE, who, "with 8-bit states eps must be 0 or at least 2^-126");
     if (!a.control && (!isfinite((float)a.lr) || !isfinite((float)a.factor) || a.step < 1))
         return refuse_call(GDN_ERR_SHAPE, who, "lr and grad_factor must be finite in fp32, step >= 1");
+    if (!a.control && !isfinite(rate_of(a)))
+        return refuse_call(GDN_ERR_SHAPE, who, "lr / (1 - beta1^step) must be finite in fp32");
     int master = -1;      // not known yet
     for (int i = 0; i < a.count; ++i) {
         const gdn_adamw_tensor& t = a.tensors[i];
@@ -396,6 +402,8 @@ int check(const Call& a)
             return refuse_call(GDN_ERR_SHAPE, who, "weight_decay must be finite and not negative");
         if (t.reserved != 0) return refuse_call(GDN_ERR_SHAPE, who, "reserved must be 0");
         if (t.n == 0) continue;
+        if (!a.control && !isfinite(decay_of(a, t)))
+            return refuse_call(GDN_ERR_SHAPE, who, "1 - lr weight_decay must be finite in fp32");
         if (!t.w || !t.g || !t.m || !t.v) return refuse_call(GDN_ERR_NULL, who, "w, g, m and v are required");
         if ((a.state_dtype == GDN_E4M3) != (t.m_scale && t.v_scale) || (a.state_dtype == GDN_F32 && (t.m_scale || t.v_scale)))
             return refuse_call(GDN_ERR_NULL, who, "8-bit states need both scales, fp32 states take none");
@@ -431,7 +439,7 @@ template <bool E8> int fill(const Call& a, int from, Pack<E8>* pk)
         Entry& e = pk->t[pk->count++];
         e.w = t.w; e.master = t.master; e.g = t.g; e.m = t.m; e.v = t.v; e.n = t.n;
         e.weight_decay = t.weight_decay;
-        e.decay = (float)(1.0 - a.lr * (double)t.weight_decay);
+        e.decay = decay_of(a, t);
         total += t.n;
     }
     // One step a workgroup (115.8 M values, fp32 states: 603 us, with two 618), or with 8-bit
@@ -452,12 +460,12 @@ template <bool E8> int fill(const Call& a, int from, Pack<E8>* pk)
 
 template <bool E8> void scalars(const Call& a, Pack<E8>* pk)
 {
-    const double c1 = 1 - pow(a.beta1, (double)a.step), c2 = 1 - pow(a.beta2, (double)a.step);
+    const double c2 = 1 - pow(a.beta2, (double)a.step);
     pk->factor = (float)a.factor;
     pk->beta1 = (float)a.beta1; pk->gain1 = (float)(1 - a.beta1);
     pk->beta2 = (float)a.beta2; pk->gain2 = (float)(1 - a.beta2);
     pk->eps = (float)a.eps;
-    pk->rate = (float)(a.lr / c1);
+    pk->rate = rate_of(a);
     pk->root = (float)(1 / sqrt(c2));
     pk->seed = a.seed;
     pk->control = a.control;
