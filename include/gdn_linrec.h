@@ -19,7 +19,8 @@
  * calls that may overlap (two streams, two captured graphs replayed at once;
  * results are then wrong or NaN).
  * Kernels only, so all can be captured into a HIP graph.  The same bits run to
- * run.  Outputs must not overlap inputs or each other (equal pointers are refused).
+ * run.  Outputs must not overlap inputs or each other (equal pointers are refused;
+ * gdn_linrec_step_plan compares no addresses).
  */
 #ifndef GDN_LINREC_H
 #define GDN_LINREC_H
@@ -94,7 +95,8 @@ int gdn_linrec_backward_plan(const void* x, const void* log_a, const void* y, co
  * and written once; row b of x, log_a and y is its token.  A NULL entry is a
  * padding row: nothing of it is read, and its row of y is left as it was.  The
  * entries that are not NULL must differ, and point at multiples of 4 bytes.
- * Limits: 1 <= B <= 65535, 1 <= D <= 2^20.
+ * Limits: 1 <= B <= 65535, 1 <= D <= 2^20.  Returns GDN_OK, GDN_ERR_NULL,
+ * GDN_ERR_SHAPE, GDN_ERR_DIM_LIMIT (D), GDN_ERR_DTYPE, GDN_ERR_STRIDE or GDN_ERR_HIP.
  */
 int gdn_linrec_step(float* const* h_table, const void* x, const void* log_a, void* y, int B, int D,
                     int64_t x_stride, int64_t a_stride, int64_t y_stride, int input_scale, int io_dtype,

@@ -188,6 +188,9 @@ int gdn_linrec_step(float* const* h_table, const void* x, const void* log_a, voi
     const int st = gdn_linrec_step_plan(h_table, x, log_a, y, B, D, x_stride, a_stride, y_stride, input_scale,
                                         io_dtype, gate_dtype);
     if (st != GDN_OK) return st;
+    // (the plan compares no addresses; a row of y written over x or log_a of another workgroup would be read there)
+    if (y == x || y == log_a || y == static_cast<const void*>(h_table))
+        return refuse_call(GDN_ERR_SHAPE, "gdn_linrec_step", "y must not share memory with h_table, x or log_a");
     return gdn::launch_status(gdn::launch_linrec_step(
         step_args(h_table, x, log_a, y, B, D, x_stride, a_stride, y_stride, input_scale, io_dtype, gate_dtype), stream));
 }
