@@ -48,13 +48,21 @@ def _lib():
 
 # ---- entry points, same names as the C ABI ----------------------------------
 
+def _ints(B, T, D):
+    """Sizes that the C call takes as ints (ctypes would cut them to 32 bits)."""
+    if max(B, T, D) > 0x7fffffff:
+        raise ValueError("B, T and D must fit in 32 bits")
+
+
 def gdn_linrec_workspace_bytes(B, T, D, packed=False) -> int:
+    _ints(B, T, D)
     return _lib().gdn_linrec_workspace_bytes(B, T, D, int(bool(packed)))
 
 
 def gdn_linrec_forward(x, log_a, h0, y, h_final, B, T, D, x_stride, a_stride, y_stride, cu_seqlens=None,
                        input_scale=LINREC_PLAIN, workspace=None, stream=None):
     """Enqueue one recurrence over sequences (layouts in include/gdn_linrec.h).  Returns the route line."""
+    _ints(B, T, D)
     if y.dtype != x.dtype:
         raise TypeError("x and y must have one dtype")
     c = _Call(x)
@@ -69,6 +77,7 @@ def gdn_linrec_backward(x, log_a, y, h0, dy, dh_final, dx, dlog_a, dh0, B, T, D,
                         dy_stride, dx_stride, da_stride, cu_seqlens=None, input_scale=LINREC_PLAIN, workspace=None,
                         stream=None):
     """Enqueue the gradients of one recurrence; x may be None with LINREC_PLAIN.  Returns the route line."""
+    _ints(B, T, D)
     dt = dy.dtype
     if y.dtype is not dt or dx.dtype is not dt or (x is not None and x.dtype is not dt):
         raise TypeError("x, y, dy and dx must have one dtype")
@@ -86,6 +95,7 @@ def gdn_linrec_backward(x, log_a, y, h0, dy, dh_final, dx, dlog_a, dh0, B, T, D,
 def gdn_linrec_step(h_table, x, log_a, y, B, D, x_stride, a_stride, y_stride, input_scale=LINREC_PLAIN, stream=None):
     """Enqueue one token of B sequences, states in place through h_table (int64 tensor of
     device pointers, 0 for a padding row).  Returns the route line."""
+    _ints(B, 0, D)
     if y.dtype != x.dtype:
         raise TypeError("x and y must have one dtype")
     c = _Call(x)
@@ -122,8 +132,11 @@ def _rows(t, lead):
 def _sizes(x, cu_seqlens):
     if cu_seqlens is not None:
         T, D = x.shape
-        return cu_seqlens.numel() - 1, T, D
-    return x.shape
+        B = cu_seqlens.numel() - 1
+    else:
+        B, T, D = x.shape
+    _ints(B, T, D)
+    return B, T, D
 
 
 def linrec_forward(x, log_a, h0=None, cu_seqlens=None, input_scale="plain", want_state=True, stream=None):
@@ -170,6 +183,7 @@ def linrec_step(h_table, x, log_a, input_scale="plain", stream=None):
     """One token x [B, D] of B sequences whose states h_table [B] points at, in place.
     Returns y [B, D]; padding rows (a pointer 0) are zeros in it."""
     B, D = x.shape
+    _ints(B, 0, D)
     _shaped(h_table=(h_table, (B,)), log_a=(log_a, x.shape))
     with _gdn._on_stream(stream, x.device):
         y = torch.zeros((B, D), dtype=x.dtype, device=x.device)

@@ -23,3 +23,27 @@ def test_step_refuses_its_inputs_as_output(lib, kw):
     a.update(kw)
     assert lib.gdn_linrec_step(*a.values()) == S["GDN_ERR_SHAPE"], gdn.last_route()
     assert "share memory" in gdn.last_route()
+
+
+def test_sizes_past_32_bits_are_refused():
+    # as the C call's ints they would wrap to a short call, and leave the other rows unwritten
+    n = (1 << 32) + 1000
+    for B, T, D in ((1, n, 1), (n, 1, 1), (1, 1, n), (1, 1 << 31, 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            gdn.gdn_linrec_workspace_bytes(B, T, D)
+    x = torch.zeros(1, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.linrec_forward(x.expand(1, n, 1), x.expand(1, n, 1))
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.linrec_forward(x.expand(n, 1), x.expand(n, 1), cu_seqlens=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.linrec_backward(*[x.expand(1, n, 1)] * 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.linrec_step(torch.zeros(1, dtype=torch.int64).expand(n), x.expand(n, 1), x.expand(n, 1))
+    a = [x.expand(n, 1)] * 2
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.gdn_linrec_forward(*a, None, a[0], None, 1, n, 1, 1, 1, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.gdn_linrec_backward(None, a[0], a[0], None, a[0], None, a[0], a[0], None, 1, n, 1, 1, 1, 1, 1, 1, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn.gdn_linrec_step(torch.zeros(1, dtype=torch.int64), a[0], a[0], a[0], n, 1, 1, 1, 1)
