@@ -53,7 +53,10 @@ class AdamwTable:
     weights: fp32 or bf16, updated in place; grads: fp32 or bf16; m, v: the states, fp32, or
     float8_e4m3fn (or uint8) codes with m_scales, v_scales fp32 [ceil(n / 128)]; masters: fp32,
     with bf16 weights only; weight_decay: one number, or one for each tensor.  The table keeps
-    the tensors alive."""
+    the tensors' memory alive, and steps on that memory: a tensor that gets other memory
+    (t.data = ...) needs a new table, or set_grads, and one in a table must not be resized.  A
+    captured step keeps the addresses it was captured with: keep its table, and its gradients
+    where they are."""
 
     def __init__(self, weights, grads, m, v, masters=None, m_scales=None, v_scales=None, weight_decay=0.0):
         weights = list(weights)
@@ -97,6 +100,8 @@ class AdamwTable:
         held = [p for e in self.entries if e.n for p in (e.w, e.m, e.v, e.master, e.m_scale, e.v_scale) if p]
         if len(set(held)) < len(held):
             raise ValueError("a tensor that a step changes is in the table twice")
+        self._memory = [t.untyped_storage() for k in ("m", "v", "masters", "m_scales", "v_scales") for t in lists[k] or ()]
+        self._memory += [w.untyped_storage() for w in weights]
         self.set_grads(lists["grads"])
 
     @staticmethod
@@ -117,6 +122,7 @@ class AdamwTable:
         for e, p in zip(self.entries, ptrs):
             e.g = p
         self._lists["grads"], self.g_dtype = grads, code
+        self._grad_memory = [t.untyped_storage() for t in grads]
 
 
 def gdn_adamw_step(table, lr, beta1, beta2, eps, step, grad_factor=1.0, control=None, stochastic=False, seed=0,
