@@ -46,8 +46,8 @@ typedef struct gdn_adamw_tensor {
  *
  * state_dtype GDN_F32: m and v are kept as they are.  GDN_E4M3: the first moment
  * and the root of the second are each kept as e4m3 codes with one fp32 scale per
- * 128 values, the group's largest finite magnitude / 448 (0 where all are zero,
- * else at least 2^-126); a value is code * scale.  The root and not v, whose
+ * 128 values, the group's largest finite magnitude times fp32's 1 / 448 (0 where all
+ * are zero, else at least 2^-126); a value is code * scale.  The root and not v, whose
  * range is the square of the root's; a root above zero has a code above zero, so
  * that no m is divided by a root that was lost.  Infinities and NaN become a
  * NaN code.  The update itself uses m and v before they are rounded.
@@ -55,10 +55,11 @@ typedef struct gdn_adamw_tensor {
  * Rounding to 8 bits, and of BF16 weights without master, is to nearest even,
  * or with stochastic != 0 up with the probability that the part cut off has, by
  * 16 of the 32 bits that a hash of (seed, the tensor's place in the call, the
- * value's place in the tensor) gives: an average that moves by 1 / 1000 a step
- * never leaves an 8-bit value that it is rounded to each time, and a BF16 weight
- * loses every update below 2^-9 of it.  Give another seed each step.  (GDN_E4M3
- * states with F32 weights: the weights are not rounded.)
+ * value's place in the tensor) gives, the lower ones for m, the upper ones for the
+ * root; BF16 weights take the lower 16 of a second hash of those bits.  An average
+ * that moves by 1 / 1000 a step never leaves an 8-bit value that it is rounded to
+ * each time, and a BF16 weight loses every update below 2^-9 of it.  Give another
+ * seed each step.  (GDN_E4M3 states with F32 weights: the weights are not rounded.)
  *
  * control: NULL, or device memory of 5 words, read by the kernels in place of
  * the arguments (for captured graphs): fp32 lr, 1 - beta1^t, 1 - beta2^t, the

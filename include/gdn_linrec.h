@@ -43,6 +43,8 @@ typedef enum gdn_linrec_scale { GDN_LINREC_PLAIN = 0, GDN_LINREC_COMPLEMENT = 1,
  * log_a and dlog_a: GDN_F32 or GDN_BF16 each, but F32 rows take F32 gates only.
  * h0, h_final, dh_final, dh0: [B][D] fp32, each may be NULL (zero, or not
  * wanted).  States, decays and sums are fp32; each output is rounded once.
+ * A state that is infinite or NaN is one of both from there on until its sequence
+ * ends (runs of rows are joined by the products of their decays), no further.
  *
  * log_a <= 0, finite or -infinity (a reset: a = 0).  With PLAIN a positive one makes
  * the state grow: decays are multiplied over runs of rows of one sequence, and no such

@@ -10,7 +10,7 @@
 // takes 16-byte accesses on any address.
 //
 // Measured for 115.8 M values in 8 tensors, bf16 weights and gradients.  fp32 masters and
-// states: 603 us (3.2 GB, 5.35 TB/s: bound by HBM, at a 1 GiB copy's rate).  States in 8
+// states: 604 us (3.2 GB, 5.35 TB/s: bound by HBM; a 1 GiB copy reaches 5.12).  States in 8
 // bits, chance rounding, no masters: 255 to 262 us (1.17 GB, 4.5 TB/s); bound by the vector units,
 // about 80 instructions a value (26 of them the random bits), which keep every SIMD busy
 // nine tenths of the time.  120 tensors of up to 5120 values: 10 us, two launches on the

@@ -117,9 +117,9 @@ template <int V> __device__ __forceinline__ void store_vec(uint16_t* p, const fl
 // 1 - a within 1.5 2^-24 of itself, and a within (1 + 3 |l|) 2^-25.  Else a is off by
 // (2 + |l|) 2^-23 of itself, and 1 - a, at least 0.22, by 2^-20 of itself at most.  Without an
 // input scale a alone is wanted, and for |l| < 1/64 a cubic gives it (2^-28.6 off there, and
-// rounded once): the hardware's exp2 is 2^-24 0.69 off near 0, 2^-27 too low on the average,
-// which adds up over the 1 / (1 - a) tokens that a state lasts.  (Three multiply-adds: short
-// calls take 0.5 us more, 1168 x 5120 in bf16 12.0 us for 11.5.)  S: 0 plain, 1 complement, 2 root.
+// rounded once): the hardware's exp2 is up to 0.69 2^-24 off near 0 and 2^-27 too low on the
+// average, which adds up over the 1 / (1 - a) tokens that a state lasts.  (Five instructions a
+// value: 1168 x 5120 in bf16 takes 11.9 us for 11.3.)  S: 0 plain, 1 complement, 2 root.
 template <int S> struct Decay {
     float a, u;
     __device__ __forceinline__ explicit Decay(float l)
@@ -167,9 +167,13 @@ constexpr int kTicketWords = 32;     // from one block's ticket to the next: lin
 // Rows of a lane's run, by its channels and the direction, and R of the segment: what
 // 128 registers a lane take, so that two workgroups share a compute unit.  A forward call
 // of few rows and channels takes one segment with longer runs, a workgroup to a compute
-// unit: no maps to clear and to wait for (300 x 768 in bf16: 7.3 us, in segments 9.8; 300 x
-// 5120, where the segments fill the chip, 11.4 and 10.0; backward, whose runs need three
-// times the registers, 380 x 768: 12.8 and 11.0).
+// unit: no maps to clear and to wait for.  200 and 380 rows in fp32 take 8.7 and 9.5 us with
+// 768 channels, in segments 10.3 and 10.4; 8.8 and 9.7 for 10.5 and 10.2 with 2048, the last
+// that the rule lets in; 10.0 for 10.2 with 2560 and 10.5 for 10.4 with 5120, where the
+// segments fill the chip.  bf16 rows and gates gain with the plain scale (300 x 768: 7.8 us for
+// 9.8); with the root 300 or 500 rows take 10.2 to 10.4 either way up to 2048 channels, 10.9
+// for 10.2 with 5120.  Backward, whose runs need three times the registers, 380 x 768 took
+// 12.8 for 11.0 in segments, and has no such form.
 template <int V, bool BACK> struct RowsOf {
     static constexpr int kRuns = 64 / (kChannels / V) * kWaves;
     static constexpr int LT = V == 1 ? 8 : V == 8 ? (BACK ? 2 : 4) : BACK ? 3 : 4;
